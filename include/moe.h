@@ -80,7 +80,8 @@ int moe_device_error(moe_stream_t stream, int32_t *host_code);
  * call for what out-of-range input does there).
  * moe_checked_build: 1 in the checked library, 0 in the plain one.
  * moe_check_status: synchronizes `stream`, reads and clears the check word into *host_flags
- * (bit 1: expert id, bit 2: offsets, bit 4: permutation entry; always 0 in the plain build)
+ * (bit 1: expert id, bit 2: offsets, bit 4: permutation entry, bit 8: cache page, bit 16: rotary
+ * position; always 0 in the plain build)
  * and returns MOE_ERR_DEVICE_CHECK if any bit is set, else MOE_OK. */
 int moe_checked_build(void);
 int moe_check_status(moe_stream_t stream, int32_t *host_flags);
@@ -395,6 +396,146 @@ int moe_layer_graph_create(const moe_layer_desc *desc, const moe_layer_weights *
 int moe_layer_graph_launch(moe_layer_graph graph, moe_stream_t stream);
 /* Frees the graph (NULL is a no-op).  No replay may be pending. */
 int moe_layer_graph_destroy(moe_layer_graph graph);
+
+/* ====================================================================================
+ * The attention half of a decoder layer: rotary positions, a paged key/value cache, and attention
+ * of drafted trees and of prompts over it.  [Specter] background on GPTQ INT4: attention stays
+ * 16-bit beside the quantized experts; method steps (2)-(5): a draft advances several tokens and
+ * the target model verifies them in one pass.  The pages define no kernel for this half; the
+ * formulas below are the definition.  Same conventions as above (device pointers, 16-byte
+ * alignment, nothing allocated, host-side checks first).  Strides are in elements.
+ *
+ * Rotary positions.  A table row of position p holds rot/2 cosines then rot/2 sines of
+ * the angles p * f_i, i < rot/2, f_i = base^(-2i/rot) changed by `scaling`:
+ *   PLAIN   f_i;
+ *   LINEAR  f_i / factor (positions compressed into the trained range);
+ *   NTK     base replaced by base * factor^(rot / (rot - 2)) (the lowest frequency is compressed by
+ *           exactly factor, the highest not at all; needs rot > 2);
+ *   PARTS   "YaRN: Efficient Context Window Extension of Large Language Models" (2023): with
+ *           r_i = original * f_i / (2 pi) turns over the trained range and
+ *           g_i = clamp((r_i - 1) / (32 - 1), 0, 1):  f_i * (g_i + (1 - g_i) / factor), and
+ *           cosines and sines times 0.1 ln(factor) + 1.
+ * Angles are formed and reduced in 64 bits (at position 10^6 a 32-bit product is off by
+ * up to 0.03 radian), the table is fp32.
+ * moe_rope: pairs (a, b) of the first rot elements of every head, out = (a cos - b sin,
+ * a sin + b cos) in fp32, one rounding; interleaved != 0: pairs (2i, 2i+1), else (i, i + rot/2);
+ * the other head_dim - rot elements are copied.  inverse != 0 turns back (sin -> -sin), which is
+ * also the gradient: the rotation is orthogonal, so grad_x = inverse(grad_out).  (With PARTS the
+ * gradient also carries the table's factor, which the inverse applies as well.)
+ * x, out: (T, heads, head_dim) of dtype F16 | BF16 | F32, the last dimension contiguous, head_dim
+ * % 8 == 0, strides multiples of 16 bytes; out may be x itself with the same strides (in place), and
+ * must not overlap it otherwise.  rot even, 2 <= rot <= head_dim.  pos: int32 (T); rows of
+ * positions outside [0, n_pos) get NaN in their rotated part (checked build: bit 16).
+ * ==================================================================================== */
+typedef enum { MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_NTK = 2, MOE_ROPE_PARTS = 3 } moe_rope_scaling;
+int moe_rope_table(int64_t n_pos, int64_t rot, double base, int scaling, double factor, int64_t original,
+                   float *cos_sin, moe_stream_t stream);
+int moe_rope(const void *x, int dtype, int64_t T, int64_t heads, int64_t head_dim, int64_t x_token_stride,
+             int64_t x_head_stride, const int32_t *pos, const float *cos_sin, int64_t n_pos, int64_t rot,
+             int interleaved, int inverse, void *out, int64_t out_token_stride, int64_t out_head_stride,
+             moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Paged key/value cache.  pool: (layers, pages, 2, kv_heads, page_size, head_dim) dtype F16 | BF16,
+ * K at index 0 and V at index 1 of the third dimension (a head's slots of one page are contiguous).
+ * One table serves every layer: table int32 (slots, max_pages) holds the page of each page_size piece of
+ * a sequence, -1 past its last; lens int32 (slots) tokens held; refs int32 (pages) how many
+ * sequences hold a page, 0 = free.  page_size a power of two in [8, 256], head_dim % 8 == 0 and
+ * <= 256, max_pages < 2^20, slots * max_pages < 2^31, pages < 2^30.  An empty cache: table all -1, lens and refs all 0.
+ * Everything is decided on the device (no host synchronization, capturable) and is independent of
+ * the launch configuration: pages are taken lowest first.
+ *
+ * Slot ids outside [0, slots) are skipped; a slot must not be named twice in one call, except as
+ * the source of a fork.  Table entries outside [0, pages) are never followed (checked build: bit 8).
+ *
+ * moe_kv_extend: grow n sequences by n_new[i] >= 0 tokens.  start[i] = the length before.  Pages are
+ *   taken in the order of (i, place in the sequence), always the lowest-numbered free one.  A
+ *   partly filled last page that other sequences hold too is replaced by a copy (all layers) before
+ *   it is written to; a page all of whose holders do so in one call ends up free.  All or
+ *   nothing: if the free pages do not suffice or a sequence would pass max_pages, nothing changes and
+ *   every start[i] is -1.  start[i] = -1 too for a skipped slot or n_new[i] < 0.  The later calls
+ *   skip sequences whose start is negative.
+ * moe_kv_fork: slot dst[i], which must be empty (else the pair is skipped), becomes a copy of
+ *   slot src[i] that shares its pages (src[i] itself not a destination of the call).
+ * moe_kv_compact: keep some of the tokens from start[i] on.  keep[cu_keep[i] .. cu_keep[i+1]) are
+ *   ascending offsets from start[i]; the j-th is moved to offset j (K and V, every layer), the
+ *   length becomes start[i] + their number, and pages past it are released.  No entries: roll back to
+ *   start[i].  A sequence is skipped if start[i] is negative or the new length would exceed the
+ *   present one; entries out of order or past the length move nothing.  The tokens from start[i]
+ *   on must be the sequence's own: not shared by a fork made since they were written (with
+ *   entries that move; a roll back is always possible).
+ * moe_kv_free: release the sequences' pages; their slots are empty afterwards.
+ * moe_kv_copy: page src[i] -> page dst[i], every layer; no page may be both a source and a
+ *   destination or twice a destination.  Ids outside [0, pages) are skipped.
+ * moe_kv_append: write new tokens into layers [layer, layer + n_layers).  Row r of sequence i,
+ *   cu[i] <= r < cu[i+1], goes to position start[i] + r - cu[i].  k, v: (n_layers, T, kv_heads,
+ *   head_dim), token and layer strides given (multiples of 8), heads contiguous.  With cos_sin
+ *   != NULL K is rotated on its way (moe_rope's arithmetic and arguments), and with q != NULL
+ *   (then n_layers must be 1) q (T, q_heads, head_dim) is rotated into q_out (contiguous; may not be q).
+ *   Rows of skipped sequences and positions past the table write no K or V.
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+  int64_t layers, pages, page_size, kv_heads, head_dim;
+  int64_t slots, max_pages;
+  int32_t dtype;
+} moe_kv_desc;
+typedef struct {
+  void *pool;
+  int32_t *table, *lens, *refs;
+} moe_kv;
+typedef struct {
+  const void *k, *v;
+  int64_t k_token_stride, k_layer_stride, v_token_stride, v_layer_stride;
+  const int32_t *cu, *seqs, *start;   /* int32 (n + 1), (n), (n) */
+  int64_t n, T;
+  const float *cos_sin;               /* NULL: no rotation */
+  const int32_t *pos;                 /* int32 (T), with cos_sin */
+  int64_t n_pos, rot;
+  int32_t interleaved;
+  const void *q;                      /* NULL: K and V only */
+  int64_t q_token_stride, q_heads;
+  void *q_out;
+} moe_kv_rows;
+size_t moe_kv_extend_workspace_size(const moe_kv_desc *desc, int64_t n);
+int moe_kv_extend(const moe_kv_desc *desc, const moe_kv *kv, const int32_t *seqs, const int32_t *n_new, int64_t n,
+                  int32_t *start, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+int moe_kv_fork(const moe_kv_desc *desc, const moe_kv *kv, const int32_t *src, const int32_t *dst, int64_t n,
+                moe_stream_t stream);
+int moe_kv_compact(const moe_kv_desc *desc, const moe_kv *kv, const int32_t *seqs, const int32_t *start,
+                   const int32_t *cu_keep, const int32_t *keep, int64_t keep_len, int64_t n, moe_stream_t stream);
+int moe_kv_free(const moe_kv_desc *desc, const moe_kv *kv, const int32_t *seqs, int64_t n, moe_stream_t stream);
+int moe_kv_copy(const moe_kv_desc *desc, const moe_kv *kv, const int32_t *src, const int32_t *dst, int64_t n,
+                moe_stream_t stream);
+int moe_kv_append(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, int64_t n_layers, const moe_kv_rows *rows,
+                  moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Attention over the cache.  n sequences; the rows cu[i] .. cu[i+1] of q are sequence seqs[i]'s new
+ * tokens, already in the cache at positions start[i] on.  Query head h reads K/V head h / (q_heads /
+ * kv_heads).  For a row and head, over its visible keys j:
+ *   s_j = scale * q . k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = ln sum_j exp(s_j).
+ * mask NULL (prompts, causal): new token t sees positions 0 .. start[i] + t.
+ * mask uint32 (T, mask_words) (a tree of drafted tokens): bit j of row r (word j / 32, bit j % 32) makes
+ *   new token j of the same sequence visible, and all positions before start[i] are; tokens from
+ *   32 * mask_words on are visible to no row.  A row without any bit is padding and sees nothing.
+ * A row that sees nothing gets out = 0 and lse = -inf.  What the cache holds where a row does not look has no
+ * influence on it, NaN and infinities included.  Sums and softmax statistics are fp32; the weights
+ * are rounded to dtype for their product with V.
+ * q: (T, q_heads, head_dim) of the cache's dtype, token stride given (a multiple of 8), heads contiguous; out:
+ * contiguous; lse: fp32 (T, q_heads) or NULL.  head_dim <= 128 here, q_heads % kv_heads == 0,
+ * q_heads / kv_heads <= 128.  Rows of no sequence are left as they were.
+ * moe_tree_mask: parents int32 (T), parents[r] = index within its sequence of row r's parent
+ *   (smaller than its own), -1 = the context; anything else makes row r and its descendants padding.
+ *   mask row: the token and its ancestors; pos[r] (may be NULL) = start[i] + depth (start[i] for
+ *   padding).  At most 32 * mask_words tokens of a sequence; later ones become padding.
+ * ------------------------------------------------------------------------------------ */
+int moe_tree_mask(const int32_t *parents, const int32_t *cu, const int32_t *start, int64_t n, int64_t T,
+                  int64_t mask_words, uint32_t *mask, int32_t *pos, moe_stream_t stream);
+size_t moe_attention_workspace_size(const moe_kv_desc *desc, int64_t T, int64_t n, int64_t q_heads);
+int moe_attention(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, const void *q, int64_t q_token_stride,
+                  int64_t q_heads, int64_t T, const int32_t *cu, const int32_t *seqs, const int32_t *start, int64_t n,
+                  const uint32_t *mask, int64_t mask_words, float scale, void *out, float *lse, void *workspace,
+                  size_t workspace_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -7,7 +7,7 @@
 #include <atomic>
 #include <cmath>
 
-#include "moe_internal.cuh"
+#include "kv_internal.cuh"
 
 namespace moe {
 
@@ -300,12 +300,17 @@ extern "C" int moe_check_status(moe_stream_t stream, int32_t *host_flags) {
   MOE_TRY(check_word_take_gemm_tc(&v));
   MOE_TRY(check_word_take_gemv(&v));
   MOE_TRY(check_word_take_gemm_mma(&v));
+  MOE_TRY(check_word_take_rope(&v));
+  MOE_TRY(check_word_take_kv(&v));
+  MOE_TRY(check_word_take_attn(&v));
   *host_flags = v;
   if (v != 0)
-    return set_error(MOE_ERR_DEVICE_CHECK, "device bounds check failed (flags 0x%x:%s%s%s)", v,
+    return set_error(MOE_ERR_DEVICE_CHECK, "device bounds check failed (flags 0x%x:%s%s%s%s%s)", v,
                      (v & kCheckExpertId) ? " expert id out of range" : "",
                      (v & kCheckOffsets) ? " expert offsets unusable" : "",
-                     (v & kCheckPerm) ? " permutation entry out of range" : "");
+                     (v & kCheckPerm) ? " permutation entry out of range" : "",
+                     (v & kCheckPage) ? " cache page out of range" : "",
+                     (v & kCheckPos) ? " rotary position out of range" : "");
   return MOE_OK;
 }
 

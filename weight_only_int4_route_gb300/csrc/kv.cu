@@ -1,0 +1,478 @@
+// Paged key/value cache: growing, forking (copy on write), compacting, freeing and copying pages, and
+// writing new tokens.
+//
+// The free pages are those nobody holds (refs == 0) and allocation takes the lowest-numbered ones in
+// the order (sequence of the call, place in the sequence): no free list whose order would depend on
+// the order of atomic pushes, so every result is the same on every run and any launch shape.
+#include "kv_internal.cuh"
+
+namespace moe {
+
+MOE_DEFINE_CHECK_WORD(kv)
+
+int check_kv_desc(const moe_kv_desc *d) {
+  MOE_REQUIRE(d != nullptr, "desc is NULL");
+  MOE_REQUIRE(is16(d->dtype), "desc.dtype must be MOE_F16 or MOE_BF16");
+  MOE_REQUIRE(d->layers >= 1 && d->layers <= 4096, "need 1 <= layers <= 4096 (%lld)", (long long)d->layers);
+  MOE_REQUIRE(d->pages >= 1 && d->pages < (int64_t(1) << 30), "need 1 <= pages < 2^30 (%lld)", (long long)d->pages);
+  MOE_REQUIRE(is_pow2(d->page_size) && d->page_size >= 8 && d->page_size <= 256,
+              "page_size must be a power of two in [8, 256] (%lld)", (long long)d->page_size);
+  MOE_REQUIRE(d->kv_heads >= 1 && d->kv_heads <= 1024, "need 1 <= kv_heads <= 1024 (%lld)", (long long)d->kv_heads);
+  MOE_REQUIRE(d->head_dim >= 8 && d->head_dim % 8 == 0 && d->head_dim <= 256,
+              "head_dim must be a multiple of 8, at most 256 (%lld)", (long long)d->head_dim);
+  MOE_REQUIRE(d->slots >= 1 && d->slots < (int64_t(1) << 30) && d->max_pages >= 1 && d->max_pages < (int64_t(1) << 20) &&
+                  d->slots * d->max_pages < (int64_t(1) << 31),
+              "need slots >= 1, 1 <= max_pages < 2^20, slots * max_pages < 2^31");
+  return MOE_OK;
+}
+
+int check_kv(const moe_kv_desc *d, const moe_kv *kv) {
+  MOE_TRY(check_kv_desc(d));
+  MOE_REQUIRE(kv && kv->pool && kv->table && kv->lens && kv->refs, "null pointer argument");
+  MOE_REQUIRE(aligned16(kv->pool) && aligned16(kv->table) && aligned16(kv->lens) && aligned16(kv->refs),
+              "pointers must be 16-byte aligned");
+  return MOE_OK;
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBook = 1024;   // threads of the one-block bookkeeping kernel
+
+// Page `p` of the table, or -1 where it must not be followed.
+__device__ __forceinline__ int valid_page(const KvView &c, int p) {
+  if (p >= 0 && p < c.pages) return p;
+  if (MOE_CHECKED && p != -1) check_fail(kCheckPage);
+  return -1;
+}
+
+__device__ __forceinline__ int pages_for(const KvView &c, int64_t len) {
+  return int((len + c.page_size() - 1) >> c.page_shift);
+}
+
+// One holder less of page p (never below zero).
+__device__ __forceinline__ void release(const KvView &c, int p) {
+  if ((p = valid_page(c, p)) < 0) return;
+  if (atomicSub(&c.refs[p], 1) <= 0) atomicAdd(&c.refs[p], 1);
+}
+
+// Where a sequence starts to take pages, and whether its partly filled last page must be copied.
+struct Growth {
+  int slot, old, want, first, shared;   // shared: the page to copy or -1; slot -1: skipped
+};
+__device__ __forceinline__ Growth growth(const KvView &c, const int32_t *seqs, const int32_t *n_new, int i) {
+  Growth g{-1, 0, 0, 0, -1};
+  const int q = seqs[i], add = n_new[i];
+  if (q < 0 || q >= c.slots || add < 0) return g;
+  const int len = c.lens[q];
+  if (len < 0) return g;
+  g.slot = q;
+  g.old = len;
+  const int have = pages_for(c, len);
+  g.want = pages_for(c, int64_t(len) + add);
+  g.first = have;
+  if (add > 0 && (len & (c.page_size() - 1)) != 0 && have <= c.max_pages) {
+    const int p = valid_page(c, c.table[int64_t(q) * c.max_pages + have - 1]);
+    if (p >= 0 && c.refs[p] > 1) {
+      g.first = have - 1;
+      g.shared = p;
+    }
+  }
+  return g;
+}
+
+// Workspace of extend: prefix[n + 1] of the pages each sequence needs, cow[2 n] (source, copy) pairs,
+// page[pages] the pages taken.
+struct ExtendWs {
+  int32_t *prefix, *cow, *page;
+};
+
+// One block: needs and their prefix sum, the lowest free pages, then tables, counts and lengths.
+__global__ void __launch_bounds__(kBook) kv_extend_kernel(const KvView c, const int32_t *__restrict__ seqs,
+                                                          const int32_t *__restrict__ n_new, int n,
+                                                          int32_t *__restrict__ start, const ExtendWs w) {
+  pdl_enter();
+  __shared__ int scratch[32];
+  __shared__ int fits;
+  const int tid = threadIdx.x;
+  if (tid == 0) fits = 1;
+  __syncthreads();
+  int total = 0;
+  for (int i0 = 0; i0 < n; i0 += kBook) {
+    const int i = i0 + tid;
+    int need = 0, at = 0;
+    if (i < n) {
+      const Growth g = growth(c, seqs, n_new, i);
+      if (g.slot >= 0) {
+        if (g.want > c.max_pages) fits = 0;
+        else need = max(0, g.want - g.first);
+      }
+    }
+    const int sum = block_exclusive_scan(min(need, c.pages + 1), &at, scratch);
+    if (i < n) w.prefix[i] = total + at;
+    total += sum;
+    if (total > c.pages) break;   // more than there are (and keeps the sums small)
+  }
+  if (tid == 0) w.prefix[n] = total;
+  __syncthreads();
+  int found = 0;
+  if (fits && total <= c.pages) {
+    for (int p0 = 0; p0 < c.pages && found < total; p0 += kBook) {
+      const int p = p0 + tid;
+      const int is_free = p < c.pages && c.refs[p] == 0;
+      int at = 0;
+      const int sum = block_exclusive_scan(is_free, &at, scratch);
+      if (is_free && found + at < total) w.page[found + at] = p;
+      found += sum;
+    }
+  }
+  __syncthreads();
+  const bool ok = fits && total <= c.pages && found >= total;
+  // decisions first (they read lens, table and refs), then the changes
+  for (int i = tid; i < n; i += kBook) {
+    const Growth g = growth(c, seqs, n_new, i);
+    start[i] = ok && g.slot >= 0 ? g.old : -1;
+    const bool copy = ok && g.shared >= 0;
+    w.cow[2 * i] = copy ? g.shared : -1;
+    w.cow[2 * i + 1] = copy ? w.page[w.prefix[i]] : -1;
+  }
+  __syncthreads();
+  if (!ok) return;
+  for (int i = tid; i < n; i += kBook) {
+    const int q = seqs[i];
+    if (start[i] < 0) continue;
+    const int old = start[i], have = pages_for(c, old), first = w.cow[2 * i] >= 0 ? have - 1 : have;
+    const int k0 = w.prefix[i], k1 = w.prefix[i + 1];
+    for (int k = k0; k < k1; ++k) {
+      c.table[int64_t(q) * c.max_pages + first + (k - k0)] = w.page[k];
+      c.refs[w.page[k]] = 1;
+    }
+    if (w.cow[2 * i] >= 0) atomicSub(&c.refs[w.cow[2 * i]], 1);
+    c.lens[q] = old + n_new[i];
+  }
+}
+
+// Page src -> page dst on every layer.  grid: (pieces of a page, layers, pairs)
+__device__ __forceinline__ void copy_page(const KvView &c, int src, int dst) {
+  const int64_t per = 2 * c.half_elems() / 8;   // 16-byte vectors of a page
+  const uint4 *s = reinterpret_cast<const uint4 *>(c.pool + int64_t(blockIdx.y) * c.layer_elems()) + src * per;
+  uint4 *d = reinterpret_cast<uint4 *>(c.pool + int64_t(blockIdx.y) * c.layer_elems()) + dst * per;
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < per; i += int64_t(gridDim.x) * blockDim.x) d[i] = s[i];
+}
+
+__global__ void __launch_bounds__(kThreads) kv_cow_kernel(const KvView c, const int32_t *__restrict__ cow, int n) {
+  pdl_enter();
+  for (int i = blockIdx.z; i < n; i += gridDim.z)
+    if (cow[2 * i] >= 0) copy_page(c, cow[2 * i], cow[2 * i + 1]);
+}
+
+__global__ void __launch_bounds__(kThreads) kv_copy_kernel(const KvView c, const int32_t *__restrict__ src,
+                                                           const int32_t *__restrict__ dst, int n) {
+  pdl_enter();
+  for (int i = blockIdx.z; i < n; i += gridDim.z) {
+    const int s = valid_page(c, src[i]), d = valid_page(c, dst[i]);
+    if (s >= 0 && d >= 0 && s != d) copy_page(c, s, d);
+  }
+}
+
+// One block per pair.
+__global__ void __launch_bounds__(kThreads) kv_fork_kernel(const KvView c, const int32_t *__restrict__ src,
+                                                           const int32_t *__restrict__ dst) {
+  pdl_enter();
+  const int s = src[blockIdx.x], d = dst[blockIdx.x];
+  if (s < 0 || s >= c.slots || d < 0 || d >= c.slots || s == d || c.lens[d] != 0) return;
+  const int len = c.lens[s], used = min(pages_for(c, max(len, 0)), c.max_pages);
+  __syncthreads();   // every thread has read lens[d]
+  for (int i = threadIdx.x; i < used; i += kThreads) {
+    const int p = c.table[int64_t(s) * c.max_pages + i];
+    c.table[int64_t(d) * c.max_pages + i] = p;
+    if (valid_page(c, p) >= 0) atomicAdd(&c.refs[p], 1);
+  }
+  if (threadIdx.x == 0) c.lens[d] = len;
+}
+
+__global__ void __launch_bounds__(kThreads) kv_free_kernel(const KvView c, const int32_t *__restrict__ seqs) {
+  pdl_enter();
+  const int q = seqs[blockIdx.x];
+  if (q < 0 || q >= c.slots) return;
+  const int used = min(pages_for(c, max(c.lens[q], 0)), c.max_pages);
+  __syncthreads();   // every thread has read lens[q]
+  for (int i = threadIdx.x; i < used; i += kThreads) release(c, atomicExch(&c.table[int64_t(q) * c.max_pages + i], -1));
+  if (threadIdx.x == 0) c.lens[q] = 0;
+}
+
+// What a compaction does to sequence i: slot, where it starts, how many stay.
+struct Kept {
+  int slot, start, len, k0, count;   // slot -1: skipped
+};
+__device__ __forceinline__ Kept kept(const KvView &c, const int32_t *seqs, const int32_t *start, const int32_t *cu_keep,
+                                     int64_t keep_len, int i) {
+  Kept k{-1, 0, 0, 0, 0};
+  const int q = seqs[i], s = start[i], k0 = cu_keep[i], k1 = cu_keep[i + 1];
+  if (q < 0 || q >= c.slots || s < 0 || k0 < 0 || k1 < k0 || k1 > keep_len) return k;
+  const int len = c.lens[q];
+  if (int64_t(s) + (k1 - k0) > len || pages_for(c, len) > c.max_pages) return k;
+  k.slot = q;
+  k.start = s;
+  k.len = len;
+  k.k0 = k0;
+  k.count = k1 - k0;
+  return k;
+}
+
+// Moves.  A thread owns one 16-byte piece of a row (of one layer, K or V, head) and walks the kept
+// tokens in order: entry j is read at offset keep[j] >= j and written at offset j, and no later entry
+// reads an offset already written (ascending: keep[j'] >= j' > j).  grid: (pieces, layers, sequences)
+__global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvView c, const int32_t *__restrict__ seqs,
+                                                              const int32_t *__restrict__ start,
+                                                              const int32_t *__restrict__ cu_keep,
+                                                              const int32_t *__restrict__ keep, int64_t keep_len, int n) {
+  pdl_enter();
+  const int dv = c.head_dim / 8, rows = 2 * c.kv_heads;
+  for (int i = blockIdx.z; i < n; i += gridDim.z) {
+    const Kept k = kept(c, seqs, start, cu_keep, keep_len, i);
+    if (k.slot < 0 || k.count == 0) continue;
+    const int32_t *tab = c.table + int64_t(k.slot) * c.max_pages;
+    uint16_t *layer = c.pool + int64_t(blockIdx.y) * c.layer_elems();
+    for (int e = blockIdx.x * kThreads + threadIdx.x; e < rows * dv; e += gridDim.x * kThreads) {
+      const int row = e / dv, piece = e - row * dv;   // row = (K or V) * kv_heads + head
+      auto at = [&](int pos) -> uint4 * {
+        const int p = valid_page(c, tab[pos >> c.page_shift]);
+        if (p < 0) return nullptr;
+        const int64_t slot = (int64_t(p) * rows + row) * c.page_size() + (pos & (c.page_size() - 1));
+        return reinterpret_cast<uint4 *>(layer + slot * c.head_dim) + piece;
+      };
+      for (int j = 0; j < k.count; ++j) {
+        const int from = keep[k.k0 + j];
+        if (from <= j || from >= k.len - k.start) continue;
+        uint4 *s = at(k.start + from), *d = at(k.start + j);
+        if (s && d) *d = *s;
+      }
+    }
+  }
+}
+
+// Lengths and pages after the moves.  One block per sequence.
+__global__ void __launch_bounds__(kThreads) kv_shrink_kernel(const KvView c, const int32_t *__restrict__ seqs,
+                                                             const int32_t *__restrict__ start,
+                                                             const int32_t *__restrict__ cu_keep, int64_t keep_len) {
+  pdl_enter();
+  const Kept k = kept(c, seqs, start, cu_keep, keep_len, blockIdx.x);
+  __syncthreads();   // every thread has read the length
+  if (k.slot < 0) return;
+  const int len = k.start + k.count;
+  for (int i = pages_for(c, len) + threadIdx.x; i < pages_for(c, k.len); i += kThreads)
+    release(c, atomicExch(&c.table[int64_t(k.slot) * c.max_pages + i], -1));
+  if (threadIdx.x == 0) c.lens[k.slot] = len;
+}
+
+struct Rows {
+  const uint16_t *k, *v, *q;
+  uint16_t *q_out;
+  int64_t kt, kl, vt, vl, qt;
+  const int32_t *cu, *seqs, *start, *pos;
+  const float *cos_sin;
+  int n, T, q_heads, rot, inter, layer;
+  int64_t n_pos;
+};
+
+// One thread per element of K, V (and q).  grid: (elements, layers)
+template <typename T>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const Rows r) {
+  pdl_enter();
+  const int D = c.head_dim, H = c.kv_heads, rows = 2 * H + r.q_heads;
+  const int64_t total = int64_t(r.T) * rows * D;
+  const T *k = reinterpret_cast<const T *>(r.k) + int64_t(blockIdx.y) * r.kl;
+  const T *v = reinterpret_cast<const T *>(r.v) + int64_t(blockIdx.y) * r.vl;
+  const T *q = reinterpret_cast<const T *>(r.q);
+  T *pool = reinterpret_cast<T *>(c.pool) + int64_t(r.layer + int(blockIdx.y)) * c.layer_elems();
+  for (int64_t e = int64_t(blockIdx.x) * kThreads + threadIdx.x; e < total; e += int64_t(gridDim.x) * kThreads) {
+    const int d = int(e % D), h = int((e / D) % rows), t = int(e / D / rows);
+    const bool is_q = h >= 2 * H, is_v = !is_q && h >= H;
+    const T *src = is_q ? q + t * r.qt + int64_t(h - 2 * H) * D : (is_v ? v + t * r.vt + int64_t(h - H) * D : k + t * r.kt + int64_t(h) * D);
+    T out = src[d];
+    if (r.cos_sin && !is_v && d < r.rot) {
+      const int half = r.rot / 2;
+      const int i = r.inter ? d / 2 : (d < half ? d : d - half);
+      const bool second = r.inter ? (d & 1) != 0 : d >= half;
+      const int p = r.pos[t];
+      float cs = NAN, sn = NAN;
+      if (p >= 0 && p < r.n_pos) {
+        cs = r.cos_sin[int64_t(p) * r.rot + i];
+        sn = r.cos_sin[int64_t(p) * r.rot + half + i];
+      } else if (MOE_CHECKED) {
+        check_fail(kCheckPos);
+      }
+      const float a = to_f32(src[r.inter ? 2 * i : i]), b = to_f32(src[r.inter ? 2 * i + 1 : i + half]);
+      out = from_f32<T>(second ? a * sn + b * cs : a * cs - b * sn);
+    }
+    if (is_q) {
+      reinterpret_cast<T *>(r.q_out)[(int64_t(t) * r.q_heads + (h - 2 * H)) * D + d] = out;
+      continue;
+    }
+    const int b = seq_of_row(r.cu, r.n, t);
+    if (b < 0) continue;
+    const int slot = r.seqs[b], st = r.start[b];
+    if (slot < 0 || slot >= c.slots || st < 0) continue;
+    const int64_t at = int64_t(st) + t - r.cu[b];
+    if ((at >> c.page_shift) >= c.max_pages) continue;
+    const int p = valid_page(c, c.table[int64_t(slot) * c.max_pages + (at >> c.page_shift)]);
+    if (p < 0) continue;
+    pool[((int64_t(p) * 2 * H + h) * c.page_size() + (at & (c.page_size() - 1))) * D + d] = out;
+  }
+}
+
+unsigned clamp_grid(int64_t v, int64_t most) { return unsigned(v < 1 ? 1 : (v < most ? v : most)); }
+
+int check_ids(const void *a, const void *b, int64_t n) {
+  MOE_REQUIRE(n >= 0 && n < (int64_t(1) << 22), "need 0 <= n < 2^22 (%lld)", (long long)n);
+  if (n == 0) return MOE_OK;
+  MOE_REQUIRE(a && b, "null pointer argument");
+  MOE_REQUIRE(aligned16(a) && aligned16(b), "pointers must be 16-byte aligned");
+  return MOE_OK;
+}
+
+dim3 page_grid(const KvView &c, int64_t n) {
+  return dim3(clamp_grid(cdiv(2 * c.half_elems() / 8, kThreads * 4), 64), unsigned(c.layers), clamp_grid(n, 65535));
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_kv_extend_workspace_size(const moe_kv_desc *desc, int64_t n) {
+  if (check_kv_desc(desc) != MOE_OK || n < 0 || n >= (int64_t(1) << 22)) return 0;
+  return align256(size_t(n + 1) * 4) + align256(size_t(n) * 8) + align256(size_t(desc->pages) * 4);
+}
+
+extern "C" int moe_kv_extend(const moe_kv_desc *desc, const moe_kv *kv, const int32_t *seqs, const int32_t *n_new,
+                             int64_t n, int32_t *start, void *workspace, size_t workspace_bytes, moe_stream_t stream) {
+  MOE_TRY(check_kv(desc, kv));
+  MOE_TRY(check_ids(seqs, n_new, n));
+  if (n == 0) return MOE_OK;
+  MOE_REQUIRE(start && aligned16(start), "start must be non-null and 16-byte aligned");
+  const size_t need = moe_kv_extend_workspace_size(desc, n);
+  MOE_REQUIRE(workspace && aligned16(workspace), "workspace must be non-null and 16-byte aligned");
+  if (workspace_bytes < need)
+    return set_error(MOE_ERR_WORKSPACE, "cache extend workspace %zu < %zu bytes", workspace_bytes, need);
+  const KvView c = kv_view(desc, kv);
+  char *ws = static_cast<char *>(workspace);
+  ExtendWs w{reinterpret_cast<int32_t *>(ws), reinterpret_cast<int32_t *>(ws + align256(size_t(n + 1) * 4)),
+             reinterpret_cast<int32_t *>(ws + align256(size_t(n + 1) * 4) + align256(size_t(n) * 8))};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  launch_pdl(kv_extend_kernel, dim3(1), dim3(kBook), 0, st, c, seqs, n_new, int(n), start, w);
+  MOE_TRY(check_launch("kv_extend"));
+  launch_pdl(kv_cow_kernel, page_grid(c, n), dim3(kThreads), 0, st, c, static_cast<const int32_t *>(w.cow), int(n));
+  return check_launch("kv_extend: copy on write");
+}
+
+extern "C" int moe_kv_fork(const moe_kv_desc *desc, const moe_kv *kv, const int32_t *src, const int32_t *dst, int64_t n,
+                           moe_stream_t stream) {
+  MOE_TRY(check_kv(desc, kv));
+  MOE_TRY(check_ids(src, dst, n));
+  if (n == 0) return MOE_OK;
+  launch_pdl(kv_fork_kernel, dim3(unsigned(n)), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), kv_view(desc, kv),
+             src, dst);
+  return check_launch("kv_fork");
+}
+
+extern "C" int moe_kv_free(const moe_kv_desc *desc, const moe_kv *kv, const int32_t *seqs, int64_t n, moe_stream_t stream) {
+  MOE_TRY(check_kv(desc, kv));
+  MOE_TRY(check_ids(seqs, seqs, n));
+  if (n == 0) return MOE_OK;
+  launch_pdl(kv_free_kernel, dim3(unsigned(n)), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), kv_view(desc, kv),
+             seqs);
+  return check_launch("kv_free");
+}
+
+extern "C" int moe_kv_compact(const moe_kv_desc *desc, const moe_kv *kv, const int32_t *seqs, const int32_t *start,
+                              const int32_t *cu_keep, const int32_t *keep, int64_t keep_len, int64_t n,
+                              moe_stream_t stream) {
+  MOE_TRY(check_kv(desc, kv));
+  MOE_TRY(check_ids(seqs, start, n));
+  MOE_REQUIRE(keep_len >= 0 && keep_len < (int64_t(1) << 31), "keep_len out of range");
+  if (n == 0) return MOE_OK;
+  MOE_REQUIRE(cu_keep && (keep || keep_len == 0), "null pointer argument");
+  MOE_REQUIRE(aligned16(cu_keep) && aligned16(keep), "pointers must be 16-byte aligned");
+  const KvView c = kv_view(desc, kv);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (keep_len > 0) {
+    const dim3 grid(clamp_grid(cdiv(int64_t(2) * c.kv_heads * (c.head_dim / 8), kThreads), 1024), unsigned(c.layers),
+                    clamp_grid(n, 65535));
+    launch_pdl(kv_compact_kernel, grid, dim3(kThreads), 0, st, c, seqs, start, cu_keep, keep, keep_len, int(n));
+    MOE_TRY(check_launch("kv_compact"));
+  }
+  launch_pdl(kv_shrink_kernel, dim3(unsigned(n)), dim3(kThreads), 0, st, c, seqs, start, cu_keep, keep_len);
+  return check_launch("kv_compact: pages");
+}
+
+extern "C" int moe_kv_copy(const moe_kv_desc *desc, const moe_kv *kv, const int32_t *src, const int32_t *dst, int64_t n,
+                           moe_stream_t stream) {
+  MOE_TRY(check_kv(desc, kv));
+  MOE_TRY(check_ids(src, dst, n));
+  if (n == 0) return MOE_OK;
+  const KvView c = kv_view(desc, kv);
+  launch_pdl(kv_copy_kernel, page_grid(c, n), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), c, src, dst, int(n));
+  return check_launch("kv_copy");
+}
+
+extern "C" int moe_kv_append(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, int64_t n_layers,
+                             const moe_kv_rows *rows, moe_stream_t stream) {
+  MOE_TRY(check_kv(desc, kv));
+  MOE_REQUIRE(rows != nullptr, "rows is NULL");
+  const moe_kv_rows &r = *rows;
+  MOE_REQUIRE(layer >= 0 && n_layers >= 1 && layer + n_layers <= desc->layers, "layers [%lld, %lld) are not in the cache",
+              (long long)layer, (long long)(layer + n_layers));
+  MOE_REQUIRE(r.T >= 0 && r.T < (int64_t(1) << 30), "T out of range");
+  MOE_TRY(check_ids(r.seqs, r.start, r.n));
+  MOE_REQUIRE(r.k_token_stride >= 0 && r.v_token_stride >= 0 && r.k_layer_stride >= 0 && r.v_layer_stride >= 0 &&
+                  r.k_token_stride % 8 == 0 && r.v_token_stride % 8 == 0 && r.k_layer_stride % 8 == 0 &&
+                  r.v_layer_stride % 8 == 0,
+              "strides must be non-negative multiples of 8");
+  MOE_REQUIRE(r.q == nullptr || (r.cos_sin != nullptr && n_layers == 1), "q needs cos_sin and a single layer");
+  if (r.T == 0 || (r.n == 0 && r.q == nullptr)) return MOE_OK;
+  MOE_REQUIRE(r.k && r.v && (r.cu || r.n == 0), "null pointer argument");
+  MOE_REQUIRE(aligned16(r.k) && aligned16(r.v) && aligned16(r.cu), "pointers must be 16-byte aligned");
+  if (r.cos_sin) {
+    MOE_REQUIRE(r.pos && aligned16(r.pos) && aligned16(r.cos_sin), "pos must be non-null, pos and cos_sin 16-byte aligned");
+    MOE_REQUIRE(r.rot >= 2 && r.rot % 2 == 0 && r.rot <= desc->head_dim, "rot must be even, 2 <= rot <= head_dim (rot=%lld)",
+                (long long)r.rot);
+    MOE_REQUIRE(r.n_pos >= 1 && r.n_pos < (int64_t(1) << 31), "n_pos out of range");
+  }
+  if (r.q) {
+    MOE_REQUIRE(r.q_heads >= 1 && r.q_heads <= 65536, "q_heads out of range");
+    MOE_REQUIRE(r.q_token_stride >= 0 && r.q_token_stride % 8 == 0, "strides must be non-negative multiples of 8");
+    MOE_REQUIRE(r.q_out && aligned16(r.q) && aligned16(r.q_out) && r.q != r.q_out,
+                "q_out must be non-null, apart from q, both 16-byte aligned");
+  }
+  const KvView c = kv_view(desc, kv);
+  Rows a{};
+  a.k = static_cast<const uint16_t *>(r.k);
+  a.v = static_cast<const uint16_t *>(r.v);
+  a.q = static_cast<const uint16_t *>(r.q);
+  a.q_out = static_cast<uint16_t *>(r.q_out);
+  a.kt = r.k_token_stride;
+  a.kl = r.k_layer_stride;
+  a.vt = r.v_token_stride;
+  a.vl = r.v_layer_stride;
+  a.qt = r.q_token_stride;
+  a.cu = r.cu;
+  a.seqs = r.seqs;
+  a.start = r.start;
+  a.pos = r.pos;
+  a.cos_sin = r.cos_sin;
+  a.n = int(r.n);
+  a.T = int(r.T);
+  a.q_heads = r.q ? int(r.q_heads) : 0;
+  a.rot = int(r.rot);
+  a.inter = r.interleaved;
+  a.layer = int(layer);
+  a.n_pos = r.n_pos;
+  const int64_t total = r.T * (2 * desc->kv_heads + a.q_heads) * desc->head_dim;
+  const dim3 grid(clamp_grid(cdiv(total, kThreads), int64_t(num_sms()) * 16), unsigned(n_layers));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (desc->dtype == MOE_F16) launch_pdl(kv_append_kernel<__half>, grid, dim3(kThreads), 0, st, c, a);
+  else launch_pdl(kv_append_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, c, a);
+  return check_launch("kv_append");
+}

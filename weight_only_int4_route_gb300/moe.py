@@ -49,6 +49,24 @@ class LayerRouting(ctypes.Structure):
     _fields_ = [("ids", _vp), ("gate_w", _vp), ("offsets", _vp), ("perm", _vp), ("inv_perm", _vp)]
 
 
+class KvDesc(ctypes.Structure):
+    _fields_ = [("layers", _c_i64), ("pages", _c_i64), ("page_size", _c_i64), ("kv_heads", _c_i64), ("head_dim", _c_i64),
+                ("slots", _c_i64), ("max_pages", _c_i64), ("dtype", ctypes.c_int32)]
+
+
+class KvPointers(ctypes.Structure):
+    _fields_ = [("pool", _vp), ("table", _vp), ("lens", _vp), ("refs", _vp)]
+
+
+class KvRows(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_token_stride", _c_i64), ("k_layer_stride", _c_i64), ("v_token_stride", _c_i64),
+                ("v_layer_stride", _c_i64), ("cu", _vp), ("seqs", _vp), ("start", _vp), ("n", _c_i64), ("T", _c_i64),
+                ("cos_sin", _vp), ("pos", _vp), ("n_pos", _c_i64), ("rot", _c_i64), ("interleaved", ctypes.c_int32),
+                ("q", _vp), ("q_token_stride", _c_i64), ("q_heads", _c_i64), ("q_out", _vp)]
+
+
+_KD, _KP = ctypes.POINTER(KvDesc), ctypes.POINTER(KvPointers)
+
 _SIGS = {
     "moe_last_error_string": (ctypes.c_char_p, []),
     "moe_version": (_c_int, []),
@@ -89,6 +107,20 @@ _SIGS = {
     "moe_layer_graph_destroy": (_c_int, [_vp]),
     "moe_layer_forward_profiled": (_c_int, [ctypes.POINTER(LayerDesc), ctypes.POINTER(LayerWeightsC), _vp, _c_i64, _vp, _vp,
                                             _c_size, _vp, ctypes.POINTER(_vp)]),
+    "moe_rope_table": (_c_int, [_c_i64, _c_i64, ctypes.c_double, _c_int, ctypes.c_double, _c_i64, _vp, _vp]),
+    "moe_rope": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _vp,
+                          _c_i64, _c_i64, _vp]),
+    "moe_kv_extend_workspace_size": (_c_size, [_KD, _c_i64]),
+    "moe_kv_extend": (_c_int, [_KD, _KP, _vp, _vp, _c_i64, _vp, _vp, _c_size, _vp]),
+    "moe_kv_fork": (_c_int, [_KD, _KP, _vp, _vp, _c_i64, _vp]),
+    "moe_kv_compact": (_c_int, [_KD, _KP, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _vp]),
+    "moe_kv_free": (_c_int, [_KD, _KP, _vp, _c_i64, _vp]),
+    "moe_kv_copy": (_c_int, [_KD, _KP, _vp, _vp, _c_i64, _vp]),
+    "moe_kv_append": (_c_int, [_KD, _KP, _c_i64, _c_i64, ctypes.POINTER(KvRows), _vp]),
+    "moe_tree_mask": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp]),
+    "moe_attention_workspace_size": (_c_size, [_KD, _c_i64, _c_i64, _c_i64]),
+    "moe_attention": (_c_int, [_KD, _KP, _c_i64, _vp, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _c_i64, _vp, _c_i64,
+                               ctypes.c_float, _vp, _vp, _vp, _c_size, _vp]),
 }
 
 # stage boundaries recorded by moe_layer_forward_profiled (enum in include/moe.h)
