@@ -273,6 +273,7 @@ extern "C" int moe_device_error(moe_stream_t stream, int32_t *host_code) {
   int v = 0;
   MOE_TRY(read_device_error(reinterpret_cast<cudaStream_t>(stream), &v));
   MOE_TRY(decode_error_take(&v));
+  MOE_TRY(attn_error_take(&v));
   *host_code = v;
   return MOE_OK;
 }

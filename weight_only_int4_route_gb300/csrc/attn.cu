@@ -3,107 +3,868 @@
 //
 //   s_j = scale q . k_j over the visible keys j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j).
 //
-// One pass over the keys with a running maximum and sum: when the maximum grows, what has been
-// summed so far is scaled down.
+// One pass over the keys in tiles of 128 on the 5th-generation tensor cores, with a running
+// maximum and sum per row.  The rows of a tile are 128 / group tokens times the group's query heads, so
+// a K/V head is read once for all its query heads; even a single token fills the 128-row MMA with
+// padding rather than take another path: per key tile the two products cost about 1100 tensor cycles,
+// where an SM's share of the memory bandwidth (64 KB a tile at head_dim 128) costs 2800.
+//
+// Two streams run through one CTA, each with its own scores, weights and output accumulator in tensor
+// memory and its own softmax warpgroup, so that one stream's products run under the other's softmax:
+//   wide    two row tiles of an item, every key tile is used by both (prompts: tensor cores bound);
+//   narrow  one row tile, the streams take alternate key tiles and are merged at the end (few rows
+//           per sequence: memory bound).
+//
+// Work: an item is (sequence, row tile or pair of them, K/V head), its units are key tiles.  The
+// units of all items, in order, are dealt to the CTAs in equal contiguous shares, whatever the lengths
+// (which only the device knows); an item cut by a share's boundary leaves partial results (running
+// maximum, sum, unscaled output) in the workspace, and a second kernel joins them in order.
+//
+// Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = row = tensor memory lane), 8 TMA (a lane per
+// page), 9 MMA issue (one thread), 10-11 idle.  Tensor memory: scores S0 S1 (128 columns each, the weights replace
+// the scores' first 64), outputs O0 O1 (head_dim columns each).
+//
+// Every wait is bounded (see mbar_wait); when one expires the CTA records a code, drains its own copies
+// and MMAs, frees its tensor memory and returns.
+#include <atomic>
+
 #include "kv_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
 MOE_DEFINE_CHECK_WORD(attn)
 
+__device__ int g_attn_error = 0;
+
+int attn_error_take(int *out) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_attn_error, sizeof(int)) != cudaSuccess) return check_launch("attention error read");
+  if (v != 0) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(int)) != cudaSuccess) return check_launch("attention error reset");
+    *out = v;
+  }
+  return MOE_OK;
+}
+
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;              // tree_mask
+constexpr int kTile = 128;                 // rows of a row tile, keys of a key tile
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kAttnThreads = 32 * 12;      // the third warpgroup: copies, MMA issue and two idle warps
+// Registers: 384 threads launch with 168 each; the softmax warpgroups (a row of 128 scores per thread)
+// take over what the third does not need: 2 x 224 + 56 = 3 x 168.
+constexpr int kSoftRegs = 224, kOtherRegs = 56;
+constexpr int kRingBytes = 128 << 10;      // K and V tiles in flight
+constexpr int kXCols = 32;                 // columns of the narrow merge's exchange buffer
+// The running maximum is only moved when a tile exceeds it by more than this (in powers of two):
+// weights grow to at most 2^8 of the largest, sums and outputs stay exact in fp32, and the
+// accumulator in tensor memory is hardly ever rescaled.
+constexpr float kLazy = 8.f;
+enum : int { kErrQ = 11, kErrKv = 12, kErrS = 13, kErrP = 14, kErrO = 15, kErrX = 16, kErrDrain = 17 };
 
 struct Rows {
-  const uint16_t *q;
-  int64_t qt;
   const int32_t *cu, *seqs, *start;
   const uint32_t *mask;
   uint16_t *out;
   float *lse;
-  int n, T, q_heads, words, layer;
+  int n, T, q_heads, group, words;
+  int tile_tokens;    // tokens of a row tile: 128 / group
   float scale_log2;   // scale * log2(e): the exponentials are taken to base 2
 };
 
-// One warp per (row, query head); a lane scores one key of 32, then owns head_dim / 32 output
-// elements for the weighted sum.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_simple_kernel(const KvView c, const Rows r) {
+// One CTA's share boundary pieces, as the joining kernel finds them.  Slot 0: the end of an item that
+// an earlier CTA began; slot 1: the beginning of an item that a later CTA ends.
+struct Piece {
+  int32_t valid, seq, tile, head, pieces, pad0, pad1, pad2;
+};
+
+struct Workspace {
+  Piece *piece;       // [2 grid]
+  float2 *ml;         // [2 grid][rows]: running maximum (to base 2), sum
+  float *o;           // [2 grid][rows][head_dim]
+};
+
+// ---------------------------------------------------------------- work
+
+// sum_{i < n} floor((a i + b) / m), by swapping the roles of the axes as in Euclid's algorithm.
+__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t sum = 0;
+  while (n > 0) {
+    if (a >= m) {
+      sum += (n - 1) * n / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// A sequence of the call: its rows and how far they look.
+struct Seq {
+  int row0, nq;       // first packed row, new tokens
+  int slot;           // table row (clamped; a skipped sequence has keys == 0)
+  int start, keys;    // cached tokens before the new ones; keys in the cache
+  int tiles;          // row tiles (of items)
+};
+__device__ __forceinline__ Seq load_seq(const KvView &c, const Rows &r, int tokens, int b) {
+  Seq s;
+  const int r0 = min(max(__ldg(r.cu + b), 0), r.T), r1 = min(max(__ldg(r.cu + b + 1), 0), r.T);
+  s.row0 = r0;
+  s.nq = max(r1 - r0, 0);
+  const int slot = __ldg(r.seqs + b), st = __ldg(r.start + b);
+  const int64_t room = int64_t(c.max_pages) << c.page_shift;   // < 2^28
+  const bool ok = slot >= 0 && slot < c.slots && st >= 0 && st <= room;
+  s.slot = ok ? slot : 0;
+  s.start = ok ? st : 0;
+  s.keys = ok ? int(min(int64_t(st) + s.nq, room)) : 0;
+  s.tiles = (s.nq + tokens - 1) / tokens;
+  return s;
+}
+// Key tiles of item row tile m.
+__device__ __forceinline__ int key_tiles(const Rows &r, const Seq &s, int tokens, int m) {
+  if (s.keys == 0) return 1;   // a skipped sequence: one tile that nobody sees
+  return r.mask ? (s.start + s.nq + kTile - 1) / kTile : (s.start + min(s.nq, (m + 1) * tokens) + kTile - 1) / kTile;
+}
+// Key tiles of item row tiles 0 .. m - 1 together.
+__device__ __forceinline__ int64_t key_tiles_before(const Rows &r, const Seq &s, int tokens, int m) {
+  if (s.keys == 0) return m;
+  if (r.mask) return int64_t(m) * ((s.start + s.nq + kTile - 1) / kTile);
+  const int full = min(m, s.tiles - 1);   // the last tile may have fewer tokens
+  int64_t n = floor_sum(full, kTile, tokens, int64_t(s.start) + tokens + kTile - 1);
+  if (m > full) n += key_tiles(r, s, tokens, s.tiles - 1);
+  return n;
+}
+
+__device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t *before, int64_t *scratch /*[32]*/) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) scratch[warp] = x;
+  __syncthreads();
+  int64_t base = 0, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp) base += scratch[w];
+    total += scratch[w];
+  }
+  __syncthreads();
+  *before = base + x - v;
+  return total;
+}
+
+// The CTA's place in the work.
+struct Place {
+  int64_t units, total;   // units of this CTA, of all
+  int seq, tile, head, key_tile;
+  int64_t item0;          // first unit of the item, counted over all
+  int64_t unit0;          // first unit of this CTA
+  int grid;               // CTAs with work
+};
+
+// Every thread of the block calls it; sh is shared.
+__device__ void find_place(const KvView &c, const Rows &r, int tokens, Place *sh, int64_t *scratch) {
+  const int tid = threadIdx.x, nt = blockDim.x, H = c.kv_heads;
+  auto units = [&](int b) -> int64_t {
+    if (b >= r.n) return 0;
+    const Seq s = load_seq(c, r, tokens, b);
+    return s.nq > 0 ? H * key_tiles_before(r, s, tokens, s.tiles) : 0;
+  };
+  int64_t v = 0, before = 0, total = 0;
+  for (int b0 = 0; b0 < r.n; b0 += nt) {
+    v = units(b0 + tid);
+    total += block_scan64(v, &before, scratch);
+  }
+  const int grid = int(min(int64_t(gridDim.x), total));
+  const int cta = blockIdx.x;
+  const int64_t u0 = cta < grid ? total * cta / grid : 0, u1 = cta < grid ? total * (cta + 1) / grid : 0;
+  if (tid == 0) {
+    sh->units = u1 - u0;
+    sh->total = total;
+    sh->grid = grid;
+    sh->unit0 = u0;
+  }
+  if (u1 > u0) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < r.n; b0 += nt) {
+      int64_t sum = total;
+      if (r.n > nt) {   // one round of threads covers the usual call: its scan is still in registers
+        v = units(b0 + tid);
+        sum = block_scan64(v, &before, scratch);
+      }
+      const int64_t at = base + before;
+      if (u0 >= at && u0 < at + v) {
+        const int b = b0 + tid;
+        const Seq s = load_seq(c, r, tokens, b);
+        int64_t off = u0 - at;
+        int lo = 0, hi = s.tiles - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (H * key_tiles_before(r, s, tokens, mid) <= off) lo = mid;
+          else hi = mid - 1;
+        }
+        off -= H * key_tiles_before(r, s, tokens, lo);
+        const int kt = key_tiles(r, s, tokens, lo);
+        sh->seq = b;
+        sh->tile = lo;
+        sh->head = int(off / kt);
+        sh->key_tile = int(off % kt);
+        sh->item0 = u0 - sh->key_tile;
+      }
+      base += sum;
+    }
+  }
+  __syncthreads();
+}
+
+// Walks the items of the CTA's share; every warp role walks the same way.
+struct Walk {
+  int64_t left, unit;       // units left, first unit of the present piece
+  int seq, tile, head;
+  int t0, cnt, total;       // key tiles [t0, t0 + cnt) of the item's total
+  Seq s;
+  int n, heads, tokens;
+  __device__ __forceinline__ Walk(const KvView &c, const Rows &r, int tokens_, const Place &p)
+      : left(p.units), unit(p.unit0), seq(p.seq), tile(p.tile), head(p.head), t0(p.key_tile), n(r.n), heads(c.kv_heads),
+        tokens(tokens_) {
+    if (left > 0) {
+      s = load_seq(c, r, tokens, seq);
+      open(r);
+    }
+  }
+  __device__ __forceinline__ void open(const Rows &r) {
+    total = key_tiles(r, s, tokens, tile);
+    cnt = int(min(int64_t(total - t0), left));
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && cnt == total; }
+  __device__ __forceinline__ void next(const KvView &c, const Rows &r) {
+    left -= cnt;
+    unit += cnt;
+    if (left <= 0) return;
+    t0 = 0;
+    if (++head == heads) {
+      head = 0;
+      if (++tile >= s.tiles) {
+        tile = 0;
+        do {
+          ++seq;
+          s = load_seq(c, r, tokens, seq);
+        } while (s.nq == 0 && seq + 1 < n);
+      }
+    }
+    open(r);
+  }
+  // Key tiles of stream st in this piece.  wide: the row tile's own limit; narrow: alternate tiles.
+  __device__ __forceinline__ int stream_tiles(const Rows &r, bool wide, int st) const {
+    if (!wide) return (cnt + 1 - st) >> 1;
+    const int tok0 = tile * tokens + st * r.tile_tokens;
+    if (tok0 >= s.nq) return 0;
+    if (s.keys == 0 || r.mask) return cnt;
+    const int lim = (s.start + min(s.nq, tok0 + r.tile_tokens) + kTile - 1) / kTile;
+    return max(0, min(cnt, lim - t0));
+  }
+};
+
+// ---------------------------------------------------------------- tensor core pieces
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  return h2_as_u32(__floats2half2_rn(lo, hi));
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  return h2_as_u32(__floats2bfloat162_rn(lo, hi));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D (tensor memory) (+)= A (tensor memory) x B (shared memory)
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// V tile as the B operand of the second product: N = head_dim is the contiguous direction (128-byte
+// swizzled rows of 64 elements, one per key), K = keys.  Leading offset: to the next 64 elements of N;
+// stride offset: to the next 8 keys.
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= uint64_t((saddr >> 4) & 0x3FFFu);
+  d |= uint64_t((kTile * 128) >> 4) << 16;
+  d |= uint64_t(1024 >> 4) << 32;
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;
+  return d;
+}
+constexpr uint32_t kTransposeB = 1u << 16;   // instruction descriptor: B is N-major
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(su32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(su32(bar))
+      : "memory");
+}
+
+// A row of 128 scores, in one statement so that nothing uses a register before the wait.
+__device__ __forceinline__ void tc_ld_row(uint32_t taddr, float (&v)[kTile]) {
+  asm volatile(
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%128];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%128 + 32];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%128 + 64];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128 + 96];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]),
+        "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
+        "=f"(v[30]), "=f"(v[31]), "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]),
+        "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]),
+        "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]), "=f"(v[49]), "=f"(v[50]),
+        "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]), "=f"(v[57]),
+        "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63]), "=f"(v[64]),
+        "=f"(v[65]), "=f"(v[66]), "=f"(v[67]), "=f"(v[68]), "=f"(v[69]), "=f"(v[70]), "=f"(v[71]),
+        "=f"(v[72]), "=f"(v[73]), "=f"(v[74]), "=f"(v[75]), "=f"(v[76]), "=f"(v[77]), "=f"(v[78]),
+        "=f"(v[79]), "=f"(v[80]), "=f"(v[81]), "=f"(v[82]), "=f"(v[83]), "=f"(v[84]), "=f"(v[85]),
+        "=f"(v[86]), "=f"(v[87]), "=f"(v[88]), "=f"(v[89]), "=f"(v[90]), "=f"(v[91]), "=f"(v[92]),
+        "=f"(v[93]), "=f"(v[94]), "=f"(v[95]), "=f"(v[96]), "=f"(v[97]), "=f"(v[98]), "=f"(v[99]),
+        "=f"(v[100]), "=f"(v[101]), "=f"(v[102]), "=f"(v[103]), "=f"(v[104]), "=f"(v[105]), "=f"(v[106]),
+        "=f"(v[107]), "=f"(v[108]), "=f"(v[109]), "=f"(v[110]), "=f"(v[111]), "=f"(v[112]), "=f"(v[113]),
+        "=f"(v[114]), "=f"(v[115]), "=f"(v[116]), "=f"(v[117]), "=f"(v[118]), "=f"(v[119]), "=f"(v[120]),
+        "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]), "=f"(v[126]), "=f"(v[127])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Shared memory of a CTA: Q (two row tiles, or two buffers of one), the ring of K and V tiles, the
+// exchange of the narrow merge, barriers.
+template <int DP> struct Smem {
+  static constexpr int kTileBytes = kTile * DP * 2;
+  static constexpr int kStages = kRingBytes / kTileBytes;
+  static constexpr int kQ = 0, kRing = 2 * kTileBytes, kX = kRing + kRingBytes, kXml = kX + kXCols * kTile * 4,
+                       kBar = kXml + kTile * 8, kBars = 2 + 2 + 2 * kStages + 4 * 2 + 2 + 1;
+  static constexpr int kScratch = kBar + kBars * 8, kPlace = kScratch + 32 * 8, kFlags = kPlace + int(sizeof(Place));
+  static constexpr int kBytes = kFlags + 16 + 1024 /* alignment */;
+};
+static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory");
+static_assert(sizeof(Place) % 8 == 0, "flags follow the place");
+
+// Position in the ring of key tile j (of n in the piece): the order of the copies is K0 K1 V0 K2 V1 ...
+__device__ __forceinline__ int k_pos(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int v_pos(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * n - 1; }
+
+template <typename T, int DP, bool WIDE>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kv, const KvView c,
+                const Rows r, const uint16_t *layer_pool, const Workspace ws) {
   pdl_enter();
-  __shared__ float qs[kThreads / 32][128];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t item = int64_t(blockIdx.x) * (kThreads / 32) + warp;
-  if (item >= int64_t(r.T) * r.q_heads) return;
-  const int t = int(item / r.q_heads), h = int(item - int64_t(t) * r.q_heads), D = c.head_dim;
-  const int b = seq_of_row(r.cu, r.n, t);
-  if (b < 0) return;
-  const T *q = reinterpret_cast<const T *>(r.q) + t * r.qt + int64_t(h) * D;
-  for (int d = lane; d < D; d += 32) qs[warp][d] = to_f32(q[d]);
-  __syncwarp();
-  const int slot = r.seqs[b], start = r.start[b], i = t - r.cu[b], nq = r.cu[b + 1] - r.cu[b];
-  int64_t keys = 0;
-  if (slot >= 0 && slot < c.slots && start >= 0) {
-    keys = int64_t(start) + (r.mask ? nq : i + 1);
-    keys = min(keys, int64_t(c.max_pages) << c.page_shift);
+  using S = Smem<DP>;
+  constexpr int kS = S::kStages, kTB = S::kTileBytes;
+  constexpr bool kF16 = std::is_same<T, __half>::value;
+  // weights are exp2(s - max + kShift): f16 keeps small weights away from its underflow (the largest,
+  // 2^(8 + 7), stays below 65504); bf16 has fp32's range
+  constexpr float kShift = kF16 ? 7.f : 0.f;
+  extern __shared__ __align__(1024) uint8_t dsmem[];
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
+  float *xbuf = reinterpret_cast<float *>(base + S::kX);
+  float2 *xml = reinterpret_cast<float2 *>(base + S::kXml);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(base + S::kBar);
+  uint64_t *q_full = bar, *q_free = bar + 2, *kv_full = bar + 4, *kv_free = kv_full + kS, *s_full = kv_free + kS,
+           *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *x_full = o_free + 2, *x_free = x_full + 1,
+           *drain = x_free + 1;
+  int64_t *scratch = reinterpret_cast<int64_t *>(base + S::kScratch);
+  Place *place = reinterpret_cast<Place *>(base + S::kPlace);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(base + S::kFlags);
+  volatile int *poison = abort_flag + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + S::kFlags + 8);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tokens = WIDE ? 2 * r.tile_tokens : r.tile_tokens;   // tokens of an item
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_free[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_ready[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 4);
+    }
+    for (int i = 0; i < kS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_free[i], 1);
+    }
+    mbar_init(x_full, 4);
+    mbar_init(x_free, 4);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *poison = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    ws.piece[2 * blockIdx.x].valid = 0;
+    ws.piece[2 * blockIdx.x + 1].valid = 0;
   }
-  const uint32_t *bits = r.mask ? r.mask + int64_t(t) * r.words : nullptr;
-  if (r.mask) {
-    bool any = false;
-    for (int w = 0; w < r.words; ++w) any |= bits[w] != 0;
-    if (!any) keys = 0;
+  find_place(c, r, tokens, place, scratch);
+  const Place pl = *place;
+  if (pl.units == 0) return;
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(tmem_slot)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
   }
-  const int32_t *tab = c.table + int64_t(max(slot, 0)) * c.max_pages;
-  const int H = c.kv_heads, hk = h / (r.q_heads / H);
-  const T *pool = reinterpret_cast<const T *>(c.pool) + r.layer * c.layer_elems();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int ksteps = (c.head_dim + 15) / 16;   // 16-wide steps of head_dim that hold anything
+  auto wait = [&](uint64_t *b, uint32_t parity, int code) { return mbar_wait(b, parity & 1, abort_flag, code, &g_attn_error); };
+
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------ copies: a lane per page of a tile
+    const int ps = c.page_size(), per = ps < kTile ? kTile / ps : 1, box = min(ps, kTile);
+    const int halves = DP / 64;
+    uint32_t ring = 0, items = 0, issued = 0, q_issued = 0, q_bytes = uint32_t(r.tile_tokens * r.group) * 128u * halves * (WIDE ? 2u : 1u);
+    bool ok = true;
+    for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r), ++items) {
+      const int qb = WIDE ? 0 : items & 1;
+      const uint32_t quse = WIDE ? items : items >> 1;
+      if (!(ok = wait(&q_free[qb], quse + 1, kErrQ))) break;
+      if (lane == 0) {
+        mbar_expect_tx(&q_full[qb], q_bytes);
+        ++q_issued;
+        const int tok = w.s.row0 + w.tile * tokens;
+#pragma unroll
+        for (int h = 0; h < halves; ++h) {
+          const uint32_t dst = su32(base + S::kQ + qb * kTB + h * kTile * 128);
+          tma_load_3d(dst, &map_q, 64 * h, w.head * r.group, tok, &q_full[qb]);
+          if (WIDE) tma_load_3d(dst + kTB, &map_q, 64 * h, w.head * r.group, tok + r.tile_tokens, &q_full[qb]);
+        }
+      }
+      const int32_t *tab = c.table + int64_t(w.s.slot) * c.max_pages;
+      // page of this lane's part of key tile j; c.pages (outside the map: reads as zero) past the keys
+      auto page_of = [&](int j) -> int {
+        const int key = (w.t0 + j) * kTile + lane * ps;
+        if (j >= w.cnt || lane >= per || key >= w.s.keys) return c.pages;
+        const int p = __ldg(tab + (key >> c.page_shift));
+        if (p >= 0 && p < c.pages) return p;
+        if (MOE_CHECKED) check_fail(kCheckPage);
+        return c.pages;
+      };
+      auto copy = [&](int j, int pos, int page, int v) -> bool {
+        const uint32_t i = ring + pos, s = i % kS;
+        if (!wait(&kv_free[s], i / kS + 1, kErrKv)) return false;
+        if (lane == 0) mbar_expect_tx(&kv_full[s], kTB);
+        issued = i + 1;
+        __syncwarp();
+        if (lane < per) {
+          const uint32_t dst = su32(base + S::kRing + s * kTB) + lane * box * 128;
+          const int slot = ((w.t0 + j) * kTile) & (ps - 1);   // nonzero in 256-token pages only
+#pragma unroll
+          for (int h = 0; h < halves; ++h)
+            tma_load_4d(dst + h * kTile * 128, &map_kv, 64 * h, slot, w.head, 2 * page + v, &kv_full[s]);
+        }
+        return true;
+      };
+      int p0 = page_of(0), p1 = page_of(1);
+      ok = copy(0, 0, p0, 0);
+      for (int j = 0; ok && j < w.cnt; ++j) {
+        if (j + 1 < w.cnt) ok = copy(j + 1, k_pos(j + 1), p1, 0);
+        const int p2 = page_of(j + 2);
+        ok = ok && copy(j, v_pos(j, w.cnt), p0, 1);
+        p0 = p1;
+        p1 = p2;
+      }
+      ring += ok ? 2 * w.cnt : 0;
+    }
+    if (lane == 0) {   // every copy must have landed before the CTA exits, also where another role gave up
+      volatile int never = 0;
+      for (uint32_t i = issued > kS ? issued - kS : 0; i < issued; ++i)
+        mbar_wait(&kv_full[i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
+      for (uint32_t i = q_issued > 1 ? q_issued - 2 : 0; i < q_issued; ++i)
+        mbar_wait(&q_full[WIDE ? 0 : i & 1], (WIDE ? i : i >> 1) & 1, &never, kErrDrain, &g_attn_error);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------ MMA issue
+    if (lane == 0) {
+      const int bf = kF16 ? 0 : 1;
+      const uint32_t id_s = idesc_f16(bf, kTile, kTile), id_o = idesc_f16(bf, kTile, ksteps * 16) | kTransposeB;
+      uint32_t ring = 0, items = 0, np[2] = {0, 0}, no[2] = {0, 0};
+      bool ok = true;
+      for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r), ++items) {
+        const int qb = WIDE ? 0 : items & 1;
+        int n[2] = {w.stream_tiles(r, WIDE, 0), w.stream_tiles(r, WIDE, 1)};
+        ok = wait(&q_full[qb], WIDE ? items : items >> 1, kErrQ);
+        // event e: stream e & 1, its tile i = e / 2, which is key tile j of the piece
+        const int events = WIDE ? 2 * w.cnt : w.cnt;
+        auto key_tile = [&](int e) { return WIDE ? e >> 1 : e; };
+        int k_seen = -1, v_seen = -1;   // key tiles whose copies have been waited for
+        auto scores = [&](int e) -> bool {
+          const int st = e & 1, j = key_tile(e);
+          if (j > k_seen) {
+            const uint32_t i = ring + k_pos(j);
+            if (!wait(&kv_full[i % kS], i / kS, kErrKv)) return false;
+            tc_fence_after();
+            k_seen = j;
+          }
+          if ((e >> 1) < n[st]) {
+            const uint32_t kb = su32(base + S::kRing + (ring + k_pos(j)) % kS * kTB);
+            const uint64_t qd = sw128_desc(su32(base + S::kQ + (WIDE ? st : qb) * kTB)), kd = sw128_desc(kb);
+            for (int k = 0; k < ksteps; ++k) {
+              const uint64_t off = uint64_t(((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4);
+              tc_mma_ss(tmem + st * kTile, qd + off, kd + off, id_s, k != 0);
+            }
+            tc_commit(&s_full[st]);
+          }
+          if (!WIDE || st == 1) tc_commit(&kv_free[(ring + k_pos(j)) % kS]);
+          if (e + 1 == events) tc_commit(&q_free[qb]);   // the item's last scores: Q may be replaced
+          return true;
+        };
+        for (int e = 0; ok && e < 2 && e < events; ++e) ok = scores(e);
+        for (int e = 0; ok && e < events; ++e) {
+          const int st = e & 1, i = e >> 1, j = key_tile(e);
+          const uint32_t vi = ring + v_pos(j, w.cnt);
+          if (j > v_seen) {
+            if (!(ok = wait(&kv_full[vi % kS], vi / kS, kErrKv))) break;
+            v_seen = j;
+          }
+          if (i < n[st]) {
+            if (i == 0 && !(ok = wait(&o_free[st], no[st] + 1, kErrO))) break;
+            if (!(ok = wait(&p_ready[st], np[st], kErrP))) break;
+            ++np[st];
+            tc_fence_after();
+            const uint64_t vd = v_desc(su32(base + S::kRing + vi % kS * kTB));
+            for (int k = 0; k < kTile / 16; ++k)
+              tc_mma_ts(tmem + 2 * kTile + st * DP, tmem + st * kTile + 8 * k, vd + uint64_t((k * 16 * 128) >> 4), id_o,
+                        (i | k) != 0);
+            if (i + 1 == n[st]) {
+              tc_commit(&o_full[st]);
+              ++no[st];
+            }
+          }
+          if (!WIDE || st == 1) tc_commit(&kv_free[vi % kS]);
+          if (e + 2 < events) ok = scores(e + 2);
+        }
+        ring += 2 * w.cnt;
+      }
+      tc_commit(drain);
+      volatile int never = 0;
+      mbar_wait(drain, 0, &never, kErrDrain, &g_attn_error);
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
+    // ------------------------------------------------ softmax and epilogue
+    const int st = warp >> 2, q4 = warp & 3, row = q4 * 32 + lane;
+    const int tok_in = row / r.group, g = row - tok_in * r.group;
+    const uint32_t lanes = uint32_t(q4 * 32) << 16;
+    const uint32_t t_s = tmem + lanes + st * kTile, t_o = tmem + lanes + 2 * kTile + st * DP;
+    const int D = c.head_dim;
+    uint32_t ring = 0, ns = 0, no = 0, nx = 0;
+    bool ok = true;
+    for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r)) {
+      const int n = w.stream_tiles(r, WIDE, st);
+      const int tok = w.tile * tokens + (WIDE ? st * r.tile_tokens : 0) + tok_in;
+      bool live = tok_in < r.tile_tokens && tok < w.s.nq;
+      const int prow = w.s.row0 + tok;   // packed row
+      const uint32_t *bits = r.mask && live ? r.mask + int64_t(prow) * r.words : nullptr;
+      const bool valid = live;           // a row of the call; live: it sees something
+      if (bits) {
+        uint32_t any = 0;
+        for (int i = 0; i < r.words; ++i) any |= __ldg(bits + i);
+        live = any != 0;
+      }
+      const bool work = __any_sync(0xffffffffu, live);
+      // causal: keys this row sees; the tiles from `edge` on are not seen whole by every row of the stream
+      const int lim = w.s.keys == 0 ? 0 : (r.mask ? w.s.keys : min(w.s.start + tok + 1, w.s.keys));
+      const int edge = w.s.keys == 0 ? 0
+                       : (r.mask ? w.s.start : min(w.s.start + tok - tok_in + 1, w.s.keys)) / kTile;
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < n; ++i) {
+        const int j = WIDE ? i : 2 * i + st, tile = w.t0 + j;
+        if (!(ok = wait(&s_full[st], ns, kErrS))) break;
+        __syncwarp();
+        ++ns;
+        tc_fence_after();
+        if (work) {
+          float v[kTile];
+          tc_ld_row(t_s, v);
+          if (tile >= edge) {
+            const int key0 = tile * kTile;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {   // bit y: the row sees key key0 + 32 x + y
+              const int k0 = key0 + 32 * x, in = min(max(lim - k0, 0), 32);
+              uint32_t see = in >= 32 ? 0xffffffffu : (1u << in) - 1u;
+              if (r.mask) {
+                const int rel = k0 - w.s.start;   // new token of bit 0
+                uint32_t word = 0xffffffffu;
+                if (rel > -32) {
+                  const int a = rel >= 0 ? rel >> 5 : -1;
+                  const uint32_t lo = a < 0 ? 0xffffffffu : (bits && a < r.words ? __ldg(bits + a) : 0u);
+                  const uint32_t hi = bits && a + 1 < r.words ? __ldg(bits + a + 1) : 0u;
+                  word = __funnelshift_r(lo, hi, rel & 31);
+                }
+                see &= word;
+              }
+              if (!live) see = 0;
+#pragma unroll
+              for (int y = 0; y < 32; ++y) v[32 * x + y] = (see >> y) & 1u ? v[32 * x + y] : -INFINITY;
+            }
+          }
+          float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int x = 4; x < kTile; ++x) top[x & 3] = fmaxf(top[x & 3], v[x]);
+          const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * r.scale_log2;
+          const bool grow = i == 0 ? mt > m : mt > m + kLazy || (m == -INFINITY && mt > m);
+          if (i > 0 && __any_sync(0xffffffffu, grow)) {
+            // the products that have been added to O are complete: this tile's scores were issued behind them
+            const float down = grow ? ex2(m - mt) : 1.f;
+            l *= down;
+            for (int x = 0; x < ksteps * 16; x += 16) {
+              uint32_t o[16];
+              tc_ld16(t_o + x, o);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * down);
+              tc_st16(t_o + x, o);
+            }
+          }
+          if (grow) m = mt;
+          const float ref = m == -INFINITY ? 0.f : m - kShift;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t p[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+              const float a = ex2(fmaf(v[32 * x + 2 * y], r.scale_log2, -ref));
+              const float b = ex2(fmaf(v[32 * x + 2 * y + 1], r.scale_log2, -ref));
+              sum[(2 * y) & 3] += a;
+              sum[(2 * y + 1) & 3] += b;
+              p[y] = pack2<T>(a, b);
+            }
+            tc_st16(t_s + 16 * x, p);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc_wait_st();
+        }
+        if (tile >= edge) {
+          // V rows that some row must not see: what lies past the keys is zeroed, and so is
+          // what is not finite among the new tokens (0 x NaN would reach every row); rows that do
+          // see those get them added in the epilogue
+          const uint32_t vi = ring + v_pos(j, w.cnt);
+          if (!(ok = wait(&kv_full[vi % kS], vi / kS, kErrKv))) break;
+          uint8_t *vt = base + S::kRing + vi % kS * kTB + row * 128;
+          const int key = tile * kTile + row;
+          if (key >= w.s.start) {
+            const bool past = key >= w.s.keys;
+            for (int x = 0; x < DP / 8; ++x) {
+              uint4 *q = reinterpret_cast<uint4 *>(vt + (x >> 3) * kTile * 128) + ((x ^ row) & 7);
+              constexpr uint32_t kExp = kF16 ? 0x7C00u : 0x7F80u;
+              uint32_t e[4] = {q->x, q->y, q->z, q->w};
+              bool bad = past;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                if ((e[y] & kExp) == kExp) bad = true, e[y] &= 0xffff0000u;
+                if ((e[y] & (kExp << 16)) == (kExp << 16)) bad = true, e[y] &= 0x0000ffffu;
+              }
+              if (bad) {
+                if (!past) *poison = 1;
+                *q = past ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(e[0], e[1], e[2], e[3]);
+              }
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[st]);
+      }
+      if (!ok) break;
+      ring += 2 * w.cnt;
+      if (!live) {
+        m = -INFINITY;
+        l = 0.f;
+      }
+      if (n > 0) {
+        if (!(ok = wait(&o_full[st], no, kErrO))) break;
+        __syncwarp();
+        ++no;
+        tc_fence_after();
+      }
+      // the running maximum that goes with l and O as they are
+      float ref = m == -INFINITY ? -INFINITY : m - kShift;
+      float mine = 1.f, other = 0.f;   // narrow: factors of the two streams
+      const int n1 = WIDE ? 0 : w.cnt >> 1;
+      if (!WIDE && n1 > 0) {
+        if (st == 1) {
+          if (!(ok = wait(x_free, nx + 1, kErrX))) break;
+          xml[row] = make_float2(ref, l);
+        }
+      }
+      const int64_t prow_h = int64_t(prow) * r.q_heads + w.head * r.group + g;
+      const int slot = w.t0 == 0 ? 1 : 0;
+      const bool whole = w.whole();
+      const int64_t part = int64_t(2 * blockIdx.x + slot) * (WIDE ? 2 * kTile : kTile) + (WIDE ? st * kTile : 0) + row;
+      for (int x0 = 0; x0 < ksteps * 16; x0 += kXCols) {
+        float o[kXCols];
+        __syncwarp();
+        if (n > 0 && work) tc_ld32(t_o + x0, o);
+        if (n == 0 || l == 0.f) {
+#pragma unroll
+          for (int y = 0; y < kXCols; ++y) o[y] = 0.f;
+        }
+        if (!WIDE && n1 > 0) {
+          if (st == 1) {
+            if (x0 > 0 && !(ok = wait(x_free, nx + 1, kErrX))) break;
+#pragma unroll
+            for (int y = 0; y < kXCols; ++y) xbuf[y * kTile + row] = o[y];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_full);
+            ++nx;
+            continue;
+          }
+          if (!(ok = wait(x_full, nx, kErrX))) break;
+          ++nx;
+          if (x0 == 0) {
+            const float2 b = xml[row];
+            const float top = fmaxf(ref, b.x);
+            mine = ref == -INFINITY ? 0.f : ex2(ref - top);
+            other = b.x == -INFINITY ? 0.f : ex2(b.x - top);
+            l = l * mine + b.y * other;
+            ref = top;
+          }
+#pragma unroll
+          for (int y = 0; y < kXCols; ++y) o[y] = o[y] * mine + xbuf[y * kTile + row] * other;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(x_free);
+        } else if (!WIDE && st == 1) {
+          break;
+        }
+        if (valid && *poison && l != 0.f) {
+          // new tokens' values that are not finite were taken out of the second product; a row that
+          // sees one gets it here (whatever its weight, the result is the same infinity or NaN)
+          const int32_t *tab = c.table + int64_t(w.s.slot) * c.max_pages;
+          const int k1 = min(lim, (w.t0 + w.cnt) * kTile);
+          for (int key = max(w.s.start, w.t0 * kTile); key < k1; ++key) {
+            const int a = key - w.s.start;
+            if (bits && !((a >> 5) < r.words && ((__ldg(bits + (a >> 5)) >> (a & 31)) & 1u))) continue;
+            const int p = __ldg(tab + (key >> c.page_shift));
+            if (p < 0 || p >= c.pages) continue;
+            const T *vr = reinterpret_cast<const T *>(layer_pool) +
+                          ((int64_t(2 * p + 1) * c.kv_heads + w.head) * c.page_size() + (key & (c.page_size() - 1))) * D + x0;
+#pragma unroll
+            for (int y = 0; y < kXCols; ++y) {
+              const float f = x0 + y < D ? to_f32(vr[y]) : 0.f;
+              if (!(fabsf(f) < INFINITY)) o[y] += f;
+            }
+          }
+        }
+        if (valid && whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          uint32_t h[kXCols / 2];
+#pragma unroll
+          for (int y = 0; y < kXCols / 2; ++y) h[y] = pack2<T>(o[2 * y] * inv, o[2 * y + 1] * inv);
+          uint4 *dst = reinterpret_cast<uint4 *>(r.out + prow_h * D + x0);
+#pragma unroll
+          for (int y = 0; y < kXCols / 8; ++y)
+            if (x0 + 8 * y < D) dst[y] = make_uint4(h[4 * y], h[4 * y + 1], h[4 * y + 2], h[4 * y + 3]);
+        } else if (valid) {
+          float4 *dst = reinterpret_cast<float4 *>(ws.o + part * DP + x0);
+#pragma unroll
+          for (int y = 0; y < kXCols / 4; ++y) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        }
+      }
+      if (!ok) break;
+      if (valid && (WIDE || st == 0)) {
+        if (whole) {
+          if (r.lse) r.lse[prow_h] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+        } else {
+          ws.ml[part] = make_float2(ref, l);
+        }
+      }
+      if (!whole && tid == 0) {
+        // the item's last unit lies in the share of the last CTA whose first unit is before its end
+        const int64_t end = w.unit - w.t0 + w.total;
+        const int last = int((end * pl.grid + pl.total - 1) / pl.total) - 1;
+        Piece p = {1, w.seq, w.tile, w.head, last - int(blockIdx.x) + 1, 0, 0, 0};
+        ws.piece[2 * blockIdx.x + slot] = p;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (n > 0 && lane == 0) mbar_arrive(&o_free[st]);
+    }
+  }
+
+  // ---- teardown: everyone done, release tensor memory
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+}
+
+// Join the pieces of the item that CTA blockIdx.x began and did not finish, in the order of the CTAs
+// (so that runs agree).  A thread owns four columns of a row.  grid: (CTAs of the first kernel, rows)
+template <typename T, int DP, bool WIDE>
+__global__ void __launch_bounds__(256) attn_join_kernel(const KvView c, const Rows r, const Workspace ws) {
+  pdl_enter();
+  const int cta = blockIdx.x;
+  const Piece p = ws.piece[2 * cta + 1];
+  if (!p.valid) return;
+  constexpr int kRows = WIDE ? 2 * kTile : kTile, kPer = DP / 4;
+  const int tokens = WIDE ? 2 * r.tile_tokens : r.tile_tokens;
+  const Seq s = load_seq(c, r, tokens, p.seq);
+  const int x = int(blockIdx.y) * 256 + int(threadIdx.x), row = x / kPer, d = 4 * (x - row * kPer);
+  const int st = row / kTile, tok_in = (row - st * kTile) / r.group, g = row - st * kTile - tok_in * r.group;
+  const int tok = p.tile * tokens + st * r.tile_tokens + tok_in;
+  if (row >= kRows || tok_in >= r.tile_tokens || tok >= s.nq) return;
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t j0 = 0; j0 < keys; j0 += 32) {
-    const int64_t j = j0 + lane;
-    bool see = j < keys;
-    if (see && bits && j >= start) {
-      const int64_t a = j - start;
-      see = a < int64_t(r.words) * 32 && ((bits[a >> 5] >> (a & 31)) & 1u);
-    }
-    const T *krow = nullptr;
-    if (see) {
-      const int p = tab[j >> c.page_shift];
-      if (p >= 0 && p < c.pages)
-        krow = pool + ((int64_t(p) * 2 * H + hk) * c.page_size() + (j & (c.page_size() - 1))) * D;
-      else if (MOE_CHECKED) check_fail(kCheckPage);
-    }
-    float s = 0.f;
-    if (krow)
-      for (int d = 0; d < D; ++d) s = fmaf(qs[warp][d], to_f32(krow[d]), s);
-    s = see ? s * r.scale_log2 : -INFINITY;
-    float top = s;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
-    const float down = exp2f(m - base), p = exp2f(s - base);
-    l *= down;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] *= down;
-    m = mn;
-    float sum = p;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    l += sum;
-    const int64_t vofs = int64_t(H) * c.page_size() * D;   // V lies behind the page's K
-    for (int k = 0; k < 32; ++k) {
-      const float pk = __shfl_sync(0xffffffffu, p, k);
-      const T *kr = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(krow), k));
-      if (!kr) continue;   // not visible: not read
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (lane + 32 * x < D) o[x] = fmaf(pk, to_f32(kr[vofs + lane + 32 * x]), o[x]);
-    }
+#pragma unroll 4
+  for (int i = 0; i < p.pieces; ++i) {
+    const int64_t at = int64_t(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * kRows + row;
+    const float2 ml = ws.ml[at];
+    const float4 v = *reinterpret_cast<const float4 *>(ws.o + at * DP + d);
+    if (ml.y == 0.f) continue;
+    const float top = fmaxf(m, ml.x), a = m == -INFINITY ? 0.f : ex2(m - top), b = ex2(ml.x - top);
+    l = l * a + ml.y * b;
+    o[0] = o[0] * a + v.x * b;
+    o[1] = o[1] * a + v.y * b;
+    o[2] = o[2] * a + v.z * b;
+    o[3] = o[3] * a + v.w * b;
+    m = top;
   }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-  for (int x = 0; x < 4; ++x)
-    if (lane + 32 * x < D)
-      reinterpret_cast<T *>(r.out)[(int64_t(t) * r.q_heads + h) * D + lane + 32 * x] = from_f32<T>(o[x] * inv);
-  if (r.lse && lane == 0) r.lse[int64_t(t) * r.q_heads + h] = (m + log2f(l)) * 0.6931471805599453f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t at = int64_t(s.row0 + tok) * r.q_heads + p.head * r.group + g;
+  if (d < c.head_dim)
+    *reinterpret_cast<uint2 *>(r.out + at * c.head_dim + d) =
+        make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
+  if (r.lse && d == 0) r.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // One thread per row: walk up to the context, setting the bit of every ancestor.
@@ -152,6 +913,89 @@ extern "C" int moe_tree_mask(const int32_t *parents, const int32_t *cu, const in
 }
 
 namespace {
+
+struct AttnPlan {
+  int grid, dp;
+  bool wide;
+  size_t o_ml, o_o, bytes;
+};
+// Two row tiles per item when a sequence brings more rows than one tile holds on average: then
+// both streams share every key tile; with fewer rows the second row tile would be padding.
+AttnPlan plan_attention(const moe_kv_desc *d, int64_t T, int64_t n, int64_t q_heads) {
+  AttnPlan p{};
+  p.grid = num_sms();
+  p.dp = d->head_dim <= 64 ? 64 : 128;
+  p.wide = T * (q_heads / d->kv_heads) > n * kTile;
+  const size_t rows = size_t(2 * p.grid) * (p.wide ? 2 : 1) * kTile;
+  p.o_ml = align256(size_t(2 * p.grid) * sizeof(Piece));
+  p.o_o = p.o_ml + align256(rows * sizeof(float2));
+  p.bytes = p.o_o + rows * p.dp * sizeof(float);
+  return p;
+}
+
+struct AttnCall {
+  const moe_kv_desc *d;
+  const moe_kv *kv;
+  int64_t layer;
+  const void *q;
+  int64_t qt;
+  AttnPlan pl;
+  char *ws;
+  cudaStream_t st;
+};
+
+template <typename T, int DP, bool WIDE> int launch_attention_as(const AttnCall &a, const Rows &r) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return check_launch("attention: cudaGetDevice");
+  if (dev < 0 || dev >= 64) return set_error(MOE_ERR_UNSUPPORTED, "attention: device index %d >= 64", dev);
+  const KvView c = kv_view(a.d, a.kv);
+  const CUtensorMapDataType type =
+      std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  CUtensorMap mq, mk;
+  {   // q as (T, heads, head_dim): a box is a row tile, 64 elements wide
+    const cuuint64_t dims[3] = {cuuint64_t(c.head_dim), cuuint64_t(r.q_heads), cuuint64_t(r.T)};
+    const cuuint64_t strides[2] = {cuuint64_t(c.head_dim) * 2, cuuint64_t(a.qt) * 2};
+    const cuuint32_t box[3] = {64u, cuuint32_t(r.group), cuuint32_t(r.tile_tokens)};
+    const CUresult e = enc(&mq, type, 3, const_cast<void *>(a.q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (e != CUDA_SUCCESS) return set_error(MOE_ERR_CUDA, "query tensor map encode failed (%d)", int(e));
+  }
+  {   // the layer's pool as (2 pages, heads, slots, head_dim): a box is a page (half a 256-token page)
+    const cuuint64_t ps = cuuint64_t(c.page_size()), D = cuuint64_t(c.head_dim), H = cuuint64_t(c.kv_heads);
+    const cuuint64_t dims[4] = {D, ps, H, 2 * cuuint64_t(c.pages)};
+    const cuuint64_t strides[3] = {D * 2, ps * D * 2, H * ps * D * 2};
+    const cuuint32_t box[4] = {64u, cuuint32_t(ps < kTile ? ps : kTile), 1u, 1u};
+    const CUresult e = enc(&mk, type, 4, c.pool + a.layer * c.layer_elems(), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (e != CUDA_SUCCESS) return set_error(MOE_ERR_CUDA, "cache tensor map encode failed (%d)", int(e));
+  }
+  Workspace ws{reinterpret_cast<Piece *>(a.ws), reinterpret_cast<float2 *>(a.ws + a.pl.o_ml),
+               reinterpret_cast<float *>(a.ws + a.pl.o_o)};
+  auto kern = attn_kernel<T, DP, WIDE>;
+  constexpr int smem = Smem<DP>::kBytes;
+  static std::atomic<bool> attr_set[64];   // the opt-in is a per-device attribute of the kernel
+  if (!attr_set[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return check_launch("attention attribute");
+    attr_set[dev].store(true, std::memory_order_relaxed);
+  }
+  launch_pdl(kern, dim3(unsigned(a.pl.grid)), dim3(kAttnThreads), smem, a.st, mq, mk, c, r,
+             static_cast<const uint16_t *>(c.pool + a.layer * c.layer_elems()), ws);
+  MOE_TRY(check_launch("attention"));
+  constexpr int rows = WIDE ? 2 * kTile : kTile;
+  launch_pdl(attn_join_kernel<T, DP, WIDE>, dim3(unsigned(a.pl.grid), unsigned(rows * (DP / 4) / 256)), dim3(256), 0, a.st, c, r,
+             ws);
+  return check_launch("attention: join");
+}
+template <typename T> int launch_attention(const AttnCall &a, const Rows &r) {
+  if (a.pl.dp == 64) return a.pl.wide ? launch_attention_as<T, 64, true>(a, r) : launch_attention_as<T, 64, false>(a, r);
+  return a.pl.wide ? launch_attention_as<T, 128, true>(a, r) : launch_attention_as<T, 128, false>(a, r);
+}
+
 int check_attention(const moe_kv_desc *d, int64_t T, int64_t n, int64_t q_heads) {
   MOE_TRY(check_kv_desc(d));
   MOE_REQUIRE(T >= 0 && T < (int64_t(1) << 30) && n >= 0 && n < (int64_t(1) << 22), "T or n out of range");
@@ -165,20 +1009,20 @@ int check_attention(const moe_kv_desc *d, int64_t T, int64_t n, int64_t q_heads)
 }  // namespace
 
 extern "C" size_t moe_attention_workspace_size(const moe_kv_desc *desc, int64_t T, int64_t n, int64_t q_heads) {
-  if (check_attention(desc, T, n, q_heads) != MOE_OK) return 0;
-  return 0;
+  if (check_attention(desc, T, n, q_heads) != MOE_OK || T == 0 || n == 0) return 0;
+  return plan_attention(desc, T, n, q_heads).bytes;
 }
 
 extern "C" int moe_attention(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, const void *q,
                              int64_t q_token_stride, int64_t q_heads, int64_t T, const int32_t *cu, const int32_t *seqs,
                              const int32_t *start, int64_t n, const uint32_t *mask, int64_t mask_words, float scale,
                              void *out, float *lse, void *workspace, size_t workspace_bytes, moe_stream_t stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   MOE_TRY(check_kv(desc, kv));
   MOE_TRY(check_attention(desc, T, n, q_heads));
   MOE_REQUIRE(layer >= 0 && layer < desc->layers, "layer %lld is not in the cache", (long long)layer);
-  MOE_REQUIRE(q_token_stride >= 0 && q_token_stride % 8 == 0, "strides must be non-negative multiples of 8");
+  MOE_REQUIRE(q_token_stride % 8 == 0 && (T <= 1 || q_token_stride >= q_heads * desc->head_dim) &&
+                  q_token_stride < (int64_t(1) << 38),
+              "q's token stride must be a multiple of 8 that holds the heads (%lld)", (long long)q_token_stride);
   MOE_REQUIRE(mask == nullptr || (mask_words >= 1 && mask_words <= 1024), "need 1 <= mask_words <= 1024 (%lld)",
               (long long)mask_words);
   MOE_REQUIRE(scale > 0.f && scale <= 3.0e38f, "scale must be positive and finite");
@@ -187,9 +1031,11 @@ extern "C" int moe_attention(const moe_kv_desc *desc, const moe_kv *kv, int64_t 
   MOE_REQUIRE(aligned16(q) && aligned16(cu) && aligned16(seqs) && aligned16(start) && aligned16(mask) && aligned16(out) &&
                   aligned16(lse),
               "pointers must be 16-byte aligned");
+  const AttnPlan pl = plan_attention(desc, T, n, q_heads);
+  MOE_REQUIRE(workspace && aligned16(workspace), "workspace must be non-null and 16-byte aligned");
+  if (workspace_bytes < pl.bytes)
+    return set_error(MOE_ERR_WORKSPACE, "attention workspace %zu < %zu bytes", workspace_bytes, pl.bytes);
   Rows r{};
-  r.q = static_cast<const uint16_t *>(q);
-  r.qt = q_token_stride;
   r.cu = cu;
   r.seqs = seqs;
   r.start = start;
@@ -199,14 +1045,11 @@ extern "C" int moe_attention(const moe_kv_desc *desc, const moe_kv *kv, int64_t 
   r.n = int(n);
   r.T = int(T);
   r.q_heads = int(q_heads);
+  r.group = int(q_heads / desc->kv_heads);
   r.words = int(mask_words);
-  r.layer = int(layer);
+  r.tile_tokens = kTile / r.group;
   r.scale_log2 = scale * 1.4426950408889634f;
-  const int64_t blocks = cdiv(T * q_heads, kThreads / 32);
-  MOE_SUPPORT(blocks < (int64_t(1) << 31), "T * q_heads too large");
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const KvView c = kv_view(desc, kv);
-  if (desc->dtype == MOE_F16) launch_pdl(attn_simple_kernel<__half>, dim3(unsigned(blocks)), dim3(kThreads), 0, st, c, r);
-  else launch_pdl(attn_simple_kernel<__nv_bfloat16>, dim3(unsigned(blocks)), dim3(kThreads), 0, st, c, r);
-  return check_launch("attention");
+  AttnCall a{desc, kv, layer, q, T <= 1 ? q_heads * desc->head_dim : q_token_stride, pl, static_cast<char *>(workspace),
+             reinterpret_cast<cudaStream_t>(stream)};
+  return desc->dtype == MOE_F16 ? launch_attention<__half>(a, r) : launch_attention<__nv_bfloat16>(a, r);
 }

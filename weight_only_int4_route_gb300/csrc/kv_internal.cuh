@@ -11,6 +11,7 @@ enum : int { kCheckPage = 8, kCheckPos = 16 };
 int check_word_take_rope(int *out);
 int check_word_take_kv(int *out);
 int check_word_take_attn(int *out);
+int attn_error_take(int *out);   // device error word of the attention kernel
 
 inline bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 int check_kv_desc(const moe_kv_desc *d);
