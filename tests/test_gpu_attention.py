@@ -124,6 +124,8 @@ CAUSAL = [
     (B16, 4, 2, 24, 8, [300], [1]),
     (B16, 2, 1, 128, 16, [1], [9000]),
     (H16, 16, 2, 128, 32, [9, 1], [5000, 3]),
+    (B16, 8, 8, 128, 64, [1500], [0]),       # several items and several key tiles per block
+    (H16, 8, 8, 64, 16, [1100, 700, 0, 300], [130, 0, 7, 1000]),
 ]
 
 

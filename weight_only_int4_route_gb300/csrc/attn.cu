@@ -506,7 +506,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       volatile int never = 0;
       for (uint32_t i = issued > kS ? issued - kS : 0; i < issued; ++i)
         mbar_wait(&kv_full[i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
-      for (uint32_t i = q_issued > 1 ? q_issued - 2 : 0; i < q_issued; ++i)
+      constexpr uint32_t kQBufs = WIDE ? 1 : 2;   // the last fill of each buffer
+      for (uint32_t i = q_issued > kQBufs ? q_issued - kQBufs : 0; i < q_issued; ++i)
         mbar_wait(&q_full[WIDE ? 0 : i & 1], (WIDE ? i : i >> 1) & 1, &never, kErrDrain, &g_attn_error);
     }
     __syncwarp();
