@@ -57,7 +57,7 @@ constexpr int kAttnThreads = 32 * 12;      // the third warpgroup: copies, MMA i
 // Registers: 384 threads launch with 168 each; the softmax warpgroups (a row of 128 scores per thread)
 // take over what the third does not need: 2 x 224 + 56 = 3 x 168.
 constexpr int kSoftRegs = 224, kOtherRegs = 56;
-constexpr int kRingBytes = 128 << 10;      // K and V tiles in flight
+constexpr int kRingBytes = 128 << 10;      // K and V tiles in flight, half of it each
 constexpr int kXCols = 32;                 // columns of the narrow merge's exchange buffer
 // The running maximum is only moved when a tile exceeds it by more than this (in powers of two):
 // weights grow to at most 2^8 of the largest, sums and outputs stay exact in fp32, and the
@@ -306,6 +306,29 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       : "memory");
 }
 
+// One lane of the warp, the same one each time; the compiler knows that a single thread runs what follows and
+// keeps descriptors in uniform registers, where the MMA instructions take them from.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
+// The 16-wide steps of head_dim of one scores tile: both operands K-major in 64-element swizzle columns.
+template <int STEPS>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc, int steps) {
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const uint64_t off = uint64_t(((i >> 2) * kTile * 128 + (i & 3) * 32) >> 4);
+    if (i < steps) tc_mma_ss(d, q + off, k + off, idesc, i != 0);
+  }
+}
+// The eight 16-key steps of one output tile: weights in tensor memory, V N-major.
+__device__ __forceinline__ void mma_output(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, bool acc) {
+#pragma unroll
+  for (int i = 0; i < kTile / 16; ++i) tc_mma_ts(d, p + 8 * i, v + uint64_t((i * 16 * 128) >> 4), idesc, i != 0 || acc);
+}
+
 // V tile as the B operand of the second product: N = head_dim is the contiguous direction (128-byte
 // swizzled rows of 64 elements, one per key), K = keys.  Leading offset: to the next 64 elements of N;
 // stride offset: to the next 8 keys.
@@ -367,18 +390,14 @@ __device__ __forceinline__ void tc_ld_row(uint32_t taddr, float (&v)[kTile]) {
 // exchange of the narrow merge, barriers.
 template <int DP> struct Smem {
   static constexpr int kTileBytes = kTile * DP * 2;
-  static constexpr int kStages = kRingBytes / kTileBytes;
+  static constexpr int kStages = kRingBytes / kTileBytes / 2;   // of the K ring, and of the V ring
   static constexpr int kQ = 0, kRing = 2 * kTileBytes, kX = kRing + kRingBytes, kXml = kX + kXCols * kTile * 4,
-                       kBar = kXml + kTile * 8, kBars = 2 + 2 + 2 * kStages + 4 * 2 + 2 + 1;
+                       kBar = kXml + kTile * 8, kBars = 2 + 2 + 4 * kStages + 4 * 2 + 2 + 1;
   static constexpr int kScratch = kBar + kBars * 8, kPlace = kScratch + 32 * 8, kFlags = kPlace + int(sizeof(Place));
   static constexpr int kBytes = kFlags + 16 + 1024 /* alignment */;
 };
 static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory");
 static_assert(sizeof(Place) % 8 == 0, "flags follow the place");
-
-// Position in the ring of key tile j (of n in the piece): the order of the copies is K0 K1 V0 K2 V1 ...
-__device__ __forceinline__ int k_pos(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ int v_pos(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * n - 1; }
 
 template <typename T, int DP, bool WIDE>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -396,7 +415,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   float *xbuf = reinterpret_cast<float *>(base + S::kX);
   float2 *xml = reinterpret_cast<float2 *>(base + S::kXml);
   uint64_t *bar = reinterpret_cast<uint64_t *>(base + S::kBar);
-  uint64_t *q_full = bar, *q_free = bar + 2, *kv_full = bar + 4, *kv_free = kv_full + kS, *s_full = kv_free + kS,
+  uint64_t *q_full = bar, *q_free = bar + 2, *kv_full = bar + 4, *kv_free = kv_full + 2 * kS, *s_full = kv_free + 2 * kS,
            *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *x_full = o_free + 2, *x_free = x_full + 1,
            *drain = x_free + 1;
   int64_t *scratch = reinterpret_cast<int64_t *>(base + S::kScratch);
@@ -416,7 +435,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&o_full[i], 1);
       mbar_init(&o_free[i], 4);
     }
-    for (int i = 0; i < kS; ++i) {
+    for (int i = 0; i < 2 * kS; ++i) {   // K stages, then V stages
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_free[i], 1);
     }
@@ -449,7 +468,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ------------------------------------------------ copies: a lane per page of a tile
     const int ps = c.page_size(), per = ps < kTile ? kTile / ps : 1, box = min(ps, kTile);
     const int halves = DP / 64;
-    uint32_t ring = 0, items = 0, issued = 0, q_issued = 0, q_bytes = uint32_t(r.tile_tokens * r.group) * 128u * halves * (WIDE ? 2u : 1u);
+    uint32_t count[2] = {0, 0}, items = 0, q_issued = 0, q_bytes = uint32_t(r.tile_tokens * r.group) * 128u * halves * (WIDE ? 2u : 1u);
     bool ok = true;
     for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r), ++items) {
       const int qb = WIDE ? 0 : items & 1;
@@ -476,11 +495,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (MOE_CHECKED) check_fail(kCheckPage);
         return c.pages;
       };
-      auto copy = [&](int j, int pos, int page, int v) -> bool {
-        const uint32_t i = ring + pos, s = i % kS;
+      auto copy = [&](int j, int page, int v) -> bool {
+        const uint32_t i = count[v], s = v * kS + i % kS;
         if (!wait(&kv_free[s], i / kS + 1, kErrKv)) return false;
         if (lane == 0) mbar_expect_tx(&kv_full[s], kTB);
-        issued = i + 1;
+        count[v] = i + 1;
         __syncwarp();
         if (lane < per) {
           const uint32_t dst = su32(base + S::kRing + s * kTB) + lane * box * 128;
@@ -491,21 +510,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         return true;
       };
+      // in the order of their use: K0 K1 V0 K2 V1 ...
       int p0 = page_of(0), p1 = page_of(1);
-      ok = copy(0, 0, p0, 0);
+      ok = copy(0, p0, 0);
       for (int j = 0; ok && j < w.cnt; ++j) {
-        if (j + 1 < w.cnt) ok = copy(j + 1, k_pos(j + 1), p1, 0);
+        if (j + 1 < w.cnt) ok = copy(j + 1, p1, 0);
         const int p2 = page_of(j + 2);
-        ok = ok && copy(j, v_pos(j, w.cnt), p0, 1);
+        ok = ok && copy(j, p0, 1);
         p0 = p1;
         p1 = p2;
       }
-      ring += ok ? 2 * w.cnt : 0;
     }
     if (lane == 0) {   // every copy must have landed before the CTA exits, also where another role gave up
       volatile int never = 0;
-      for (uint32_t i = issued > kS ? issued - kS : 0; i < issued; ++i)
-        mbar_wait(&kv_full[i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
+      for (int v = 0; v < 2; ++v)
+        for (uint32_t i = count[v] > kS ? count[v] - kS : 0; i < count[v]; ++i)
+          mbar_wait(&kv_full[v * kS + i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
       constexpr uint32_t kQBufs = WIDE ? 1 : 2;   // the last fill of each buffer
       for (uint32_t i = q_issued > kQBufs ? q_issued - kQBufs : 0; i < q_issued; ++i)
         mbar_wait(&q_full[WIDE ? 0 : i & 1], (WIDE ? i : i >> 1) & 1, &never, kErrDrain, &g_attn_error);
@@ -513,66 +533,63 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issue
-    if (lane == 0) {
+    // Event e of a piece is stream e & 1's tile e / 2, key tile e / 2 (wide) or e (narrow): the scores of
+    // the first two events, then per event its second product and the scores of the event after next
+    // (the same stream's next tile, which may overwrite the weights just used: MMAs run in order).
+    if (elect_one()) {
       const int bf = kF16 ? 0 : 1;
       const uint32_t id_s = idesc_f16(bf, kTile, kTile), id_o = idesc_f16(bf, kTile, ksteps * 16) | kTransposeB;
-      uint32_t ring = 0, items = 0, np[2] = {0, 0}, no[2] = {0, 0};
+      const uint64_t q_desc = sw128_desc(su32(base + S::kQ)), k_desc = sw128_desc(su32(base + S::kRing)),
+                     v0_desc = v_desc(su32(base + S::kRing + kS * kTB));
+      uint32_t kc = 0, vc = 0, items = 0, np[2] = {0, 0}, no[2] = {0, 0};
       bool ok = true;
       for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r), ++items) {
         const int qb = WIDE ? 0 : items & 1;
-        int n[2] = {w.stream_tiles(r, WIDE, 0), w.stream_tiles(r, WIDE, 1)};
-        ok = wait(&q_full[qb], WIDE ? items : items >> 1, kErrQ);
-        // event e: stream e & 1, its tile i = e / 2, which is key tile j of the piece
+        const int n0 = w.stream_tiles(r, WIDE, 0), n1 = w.stream_tiles(r, WIDE, 1);
         const int events = WIDE ? 2 * w.cnt : w.cnt;
-        auto key_tile = [&](int e) { return WIDE ? e >> 1 : e; };
-        int k_seen = -1, v_seen = -1;   // key tiles whose copies have been waited for
+        ok = wait(&q_full[qb], WIDE ? items : items >> 1, kErrQ);
         auto scores = [&](int e) -> bool {
-          const int st = e & 1, j = key_tile(e);
-          if (j > k_seen) {
-            const uint32_t i = ring + k_pos(j);
-            if (!wait(&kv_full[i % kS], i / kS, kErrKv)) return false;
+          const int st = e & 1;
+          const uint32_t ks = kc % kS;
+          if (!WIDE || st == 0) {
+            if (!wait(&kv_full[ks], kc / kS, kErrKv)) return false;
             tc_fence_after();
-            k_seen = j;
           }
-          if ((e >> 1) < n[st]) {
-            const uint32_t kb = su32(base + S::kRing + (ring + k_pos(j)) % kS * kTB);
-            const uint64_t qd = sw128_desc(su32(base + S::kQ + (WIDE ? st : qb) * kTB)), kd = sw128_desc(kb);
-            for (int k = 0; k < ksteps; ++k) {
-              const uint64_t off = uint64_t(((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4);
-              tc_mma_ss(tmem + st * kTile, qd + off, kd + off, id_s, k != 0);
-            }
+          if ((e >> 1) < (st ? n1 : n0)) {
+            mma_scores<DP / 16>(tmem + st * kTile, q_desc + uint64_t((WIDE ? st : qb) * (kTB >> 4)),
+                                k_desc + uint64_t(ks * (kTB >> 4)), id_s, ksteps);
             tc_commit(&s_full[st]);
           }
-          if (!WIDE || st == 1) tc_commit(&kv_free[(ring + k_pos(j)) % kS]);
+          if (!WIDE || st == 1) {
+            tc_commit(&kv_free[ks]);
+            ++kc;
+          }
           if (e + 1 == events) tc_commit(&q_free[qb]);   // the item's last scores: Q may be replaced
           return true;
         };
         for (int e = 0; ok && e < 2 && e < events; ++e) ok = scores(e);
         for (int e = 0; ok && e < events; ++e) {
-          const int st = e & 1, i = e >> 1, j = key_tile(e);
-          const uint32_t vi = ring + v_pos(j, w.cnt);
-          if (j > v_seen) {
-            if (!(ok = wait(&kv_full[vi % kS], vi / kS, kErrKv))) break;
-            v_seen = j;
-          }
-          if (i < n[st]) {
+          const int st = e & 1, i = e >> 1, n = st ? n1 : n0;
+          const uint32_t vs = vc % kS;
+          if (!WIDE || st == 0)
+            if (!(ok = wait(&kv_full[kS + vs], vc / kS, kErrKv))) break;
+          if (i < n) {
             if (i == 0 && !(ok = wait(&o_free[st], no[st] + 1, kErrO))) break;
             if (!(ok = wait(&p_ready[st], np[st], kErrP))) break;
             ++np[st];
             tc_fence_after();
-            const uint64_t vd = v_desc(su32(base + S::kRing + vi % kS * kTB));
-            for (int k = 0; k < kTile / 16; ++k)
-              tc_mma_ts(tmem + 2 * kTile + st * DP, tmem + st * kTile + 8 * k, vd + uint64_t((k * 16 * 128) >> 4), id_o,
-                        (i | k) != 0);
-            if (i + 1 == n[st]) {
+            mma_output(tmem + 2 * kTile + st * DP, tmem + st * kTile, v0_desc + uint64_t(vs * (kTB >> 4)), id_o, i != 0);
+            if (i + 1 == n) {
               tc_commit(&o_full[st]);
               ++no[st];
             }
           }
-          if (!WIDE || st == 1) tc_commit(&kv_free[vi % kS]);
+          if (!WIDE || st == 1) {
+            tc_commit(&kv_free[kS + vs]);
+            ++vc;
+          }
           if (e + 2 < events) ok = scores(e + 2);
         }
-        ring += 2 * w.cnt;
       }
       tc_commit(drain);
       volatile int never = 0;
@@ -588,7 +605,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t lanes = uint32_t(q4 * 32) << 16;
     const uint32_t t_s = tmem + lanes + st * kTile, t_o = tmem + lanes + 2 * kTile + st * DP;
     const int D = c.head_dim;
-    uint32_t ring = 0, ns = 0, no = 0, nx = 0;
+    uint32_t tiles = 0, ns = 0, no = 0, nx = 0;   // tiles: key tiles of the pieces before
     bool ok = true;
     for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r)) {
       const int n = w.stream_tiles(r, WIDE, st);
@@ -679,9 +696,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // V rows that some row must not see: what lies past the keys is zeroed, and so is
           // what is not finite among the new tokens (0 x NaN would reach every row); rows that do
           // see those get them added in the epilogue
-          const uint32_t vi = ring + v_pos(j, w.cnt);
-          if (!(ok = wait(&kv_full[vi % kS], vi / kS, kErrKv))) break;
-          uint8_t *vt = base + S::kRing + vi % kS * kTB + row * 128;
+          const uint32_t vi = tiles + j;
+          if (!(ok = wait(&kv_full[kS + vi % kS], vi / kS, kErrKv))) break;
+          uint8_t *vt = base + S::kRing + (kS + vi % kS) * kTB + row * 128;
           const int key = tile * kTile + row;
           if (key >= w.s.start) {
             const bool past = key >= w.s.keys;
@@ -708,7 +725,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) mbar_arrive(&p_ready[st]);
       }
       if (!ok) break;
-      ring += 2 * w.cnt;
+      tiles += w.cnt;
       if (!live) {
         m = -INFINITY;
         l = 0.f;
