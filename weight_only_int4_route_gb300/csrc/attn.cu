@@ -15,13 +15,14 @@
 //   narrow  one row tile, the streams take alternate key tiles and are merged at the end (few rows
 //           per sequence: memory bound).
 //
-// Work: an item is (sequence, row tile or pair of them, K/V head), its units are key tiles.  The
-// units of all items, in order, are dealt to the CTAs in equal contiguous shares, whatever the lengths
+// Work: an item is (sequence, row tile or pair of them, K/V head), its units are kItemCost units of
+// overhead and its key tiles.  The units of all items, in order, are dealt to the CTAs in equal contiguous shares, whatever the lengths
 // (which only the device knows); an item cut by a share's boundary leaves partial results (running
 // maximum, sum, unscaled output) in the workspace, and a second kernel joins them in order.
 //
-// Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = row = tensor memory lane), 8 TMA (a lane per
-// page), 9 MMA issue (one thread), 10-11 idle.  Tensor memory: scores S0 S1 (128 columns each, the weights replace
+// Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = row = tensor memory lane), 8 copies of K and V
+// (a lane per page), 9 MMA issue (one thread), 10 copies of Q (one thread; apart from 8, so that the next
+// item's keys are under way while Q's buffer is still in use), 11 idle.  Tensor memory: scores S0 S1 (128 columns each, the weights replace
 // the scores' first 64), outputs O0 O1 (head_dim columns each).
 //
 // Every wait is bounded (see mbar_wait); when one expires the CTA records a code, drains its own copies
@@ -52,17 +53,21 @@ namespace {
 
 constexpr int kThreads = 128;              // tree_mask
 constexpr int kTile = 128;                 // rows of a row tile, keys of a key tile
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kAttnThreads = 32 * 12;      // the third warpgroup: copies, MMA issue and two idle warps
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kQWarp = 10;
+constexpr int kAttnThreads = 32 * 12;      // the third warpgroup: copies, MMA issue and an idle warp
 // Registers: 384 threads launch with 168 each; the softmax warpgroups (a row of 128 scores per thread)
 // take over what the third does not need: 2 x 224 + 56 = 3 x 168.
 constexpr int kSoftRegs = 224, kOtherRegs = 56;
 constexpr int kRingBytes = 128 << 10;      // K and V tiles in flight, half of it each
-constexpr int kXCols = 32;                 // columns of the narrow merge's exchange buffer
+constexpr int kXCols = 32;                 // columns of the output that the epilogue handles at a time
+constexpr int kStageBytes = 32 * kXCols * 2;   // a softmax warp's 16-bit output rows of those columns
 // The running maximum is only moved when a tile exceeds it by more than this (in powers of two):
 // weights grow to at most 2^8 of the largest, sums and outputs stay exact in fp32, and the
 // accumulator in tensor memory is hardly ever rescaled.
 constexpr float kLazy = 8.f;
+// What an item costs beside its key tiles (its queries, its first tiles' latency, its epilogue), in key
+// tiles: shares are dealt with it counted in.
+constexpr int kItemCost = 3;
 enum : int { kErrQ = 11, kErrKv = 12, kErrS = 13, kErrP = 14, kErrO = 15, kErrX = 16, kErrDrain = 17 };
 
 struct Rows {
@@ -84,7 +89,7 @@ struct Piece {
 struct Workspace {
   Piece *piece;       // [2 grid]
   float2 *ml;         // [2 grid][rows]: running maximum (to base 2), sum
-  float *o;           // [2 grid][rows][head_dim]
+  float *o;           // [2 grid][head_dim][rows]
 };
 
 // ---------------------------------------------------------------- work
@@ -171,10 +176,10 @@ __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t *before, int6
 // The CTA's place in the work.
 struct Place {
   int64_t units, total;   // units of this CTA, of all
-  int seq, tile, head, key_tile;
-  int64_t item0;          // first unit of the item, counted over all
+  int seq, tile, head, in_item;   // in_item: units of the first item that belong to earlier CTAs
+  int pad;
   int64_t unit0;          // first unit of this CTA
-  int grid;               // CTAs with work
+  int grid, pad2;         // CTAs with work
 };
 
 // Every thread of the block calls it; sh is shared.
@@ -183,7 +188,7 @@ __device__ void find_place(const KvView &c, const Rows &r, int tokens, Place *sh
   auto units = [&](int b) -> int64_t {
     if (b >= r.n) return 0;
     const Seq s = load_seq(c, r, tokens, b);
-    return s.nq > 0 ? H * key_tiles_before(r, s, tokens, s.tiles) : 0;
+    return s.nq > 0 ? H * (key_tiles_before(r, s, tokens, s.tiles) + int64_t(kItemCost) * s.tiles) : 0;
   };
   int64_t v = 0, before = 0, total = 0;
   for (int b0 = 0; b0 < r.n; b0 += nt) {
@@ -215,16 +220,15 @@ __device__ void find_place(const KvView &c, const Rows &r, int tokens, Place *sh
         int lo = 0, hi = s.tiles - 1;
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (H * key_tiles_before(r, s, tokens, mid) <= off) lo = mid;
+          if (H * (key_tiles_before(r, s, tokens, mid) + int64_t(kItemCost) * mid) <= off) lo = mid;
           else hi = mid - 1;
         }
-        off -= H * key_tiles_before(r, s, tokens, lo);
-        const int kt = key_tiles(r, s, tokens, lo);
+        off -= H * (key_tiles_before(r, s, tokens, lo) + int64_t(kItemCost) * lo);
+        const int kt = key_tiles(r, s, tokens, lo) + kItemCost;
         sh->seq = b;
         sh->tile = lo;
         sh->head = int(off / kt);
-        sh->key_tile = int(off % kt);
-        sh->item0 = u0 - sh->key_tile;
+        sh->in_item = int(off % kt);
       }
       base += sum;
     }
@@ -232,32 +236,36 @@ __device__ void find_place(const KvView &c, const Rows &r, int tokens, Place *sh
   __syncthreads();
 }
 
-// Walks the items of the CTA's share; every warp role walks the same way.
+// Walks the pieces of items in the CTA's share; every warp role walks the same way.
 struct Walk {
   int64_t left, unit;       // units left, first unit of the present piece
   int seq, tile, head;
-  int t0, cnt, total;       // key tiles [t0, t0 + cnt) of the item's total
+  int in_item, take;        // the piece: units [in_item, in_item + take) of the item
+  int t0, cnt, total;       // its key tiles [t0, t0 + cnt) of the item's total
   Seq s;
   int n, heads, tokens;
   __device__ __forceinline__ Walk(const KvView &c, const Rows &r, int tokens_, const Place &p)
-      : left(p.units), unit(p.unit0), seq(p.seq), tile(p.tile), head(p.head), t0(p.key_tile), n(r.n), heads(c.kv_heads),
+      : left(p.units), unit(p.unit0), seq(p.seq), tile(p.tile), head(p.head), in_item(p.in_item), n(r.n), heads(c.kv_heads),
         tokens(tokens_) {
     if (left > 0) {
       s = load_seq(c, r, tokens, seq);
       open(r);
+      if (cnt == 0) next(c, r);   // the share's first units are overhead only
     }
   }
   __device__ __forceinline__ void open(const Rows &r) {
     total = key_tiles(r, s, tokens, tile);
-    cnt = int(min(int64_t(total - t0), left));
+    take = int(min(int64_t(total + kItemCost - in_item), left));
+    t0 = max(in_item - kItemCost, 0);
+    cnt = max(in_item + take - kItemCost, 0) - t0;
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && cnt == total; }
   __device__ __forceinline__ void next(const KvView &c, const Rows &r) {
-    left -= cnt;
-    unit += cnt;
+    left -= take;
+    unit += take;
     if (left <= 0) return;
-    t0 = 0;
+    in_item = 0;
     if (++head == heads) {
       head = 0;
       if (++tile >= s.tiles) {
@@ -269,6 +277,7 @@ struct Walk {
       }
     }
     open(r);
+    if (cnt == 0) left = 0;   // only a share's last units can be overhead alone: the item is the next CTA's
   }
   // Key tiles of stream st in this piece.  wide: the row tile's own limit; narrow: alternate tiles.
   __device__ __forceinline__ int stream_tiles(const Rows &r, bool wide, int st) const {
@@ -392,7 +401,7 @@ template <int DP> struct Smem {
   static constexpr int kTileBytes = kTile * DP * 2;
   static constexpr int kStages = kRingBytes / kTileBytes / 2;   // of the K ring, and of the V ring
   static constexpr int kQ = 0, kRing = 2 * kTileBytes, kX = kRing + kRingBytes, kXml = kX + kXCols * kTile * 4,
-                       kBar = kXml + kTile * 8, kBars = 2 + 2 + 4 * kStages + 4 * 2 + 2 + 1;
+                       kStage = kXml + kTile * 8, kBar = kStage + kSoftWarps * kStageBytes, kBars = 2 + 2 + 4 * kStages + 4 * 2 + 2 + 1;
   static constexpr int kScratch = kBar + kBars * 8, kPlace = kScratch + 32 * 8, kFlags = kPlace + int(sizeof(Place));
   static constexpr int kBytes = kFlags + 16 + 1024 /* alignment */;
 };
@@ -468,23 +477,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ------------------------------------------------ copies: a lane per page of a tile
     const int ps = c.page_size(), per = ps < kTile ? kTile / ps : 1, box = min(ps, kTile);
     const int halves = DP / 64;
-    uint32_t count[2] = {0, 0}, items = 0, q_issued = 0, q_bytes = uint32_t(r.tile_tokens * r.group) * 128u * halves * (WIDE ? 2u : 1u);
+    uint32_t count[2] = {0, 0};
     bool ok = true;
-    for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r), ++items) {
-      const int qb = WIDE ? 0 : items & 1;
-      const uint32_t quse = WIDE ? items : items >> 1;
-      if (!(ok = wait(&q_free[qb], quse + 1, kErrQ))) break;
-      if (lane == 0) {
-        mbar_expect_tx(&q_full[qb], q_bytes);
-        ++q_issued;
-        const int tok = w.s.row0 + w.tile * tokens;
-#pragma unroll
-        for (int h = 0; h < halves; ++h) {
-          const uint32_t dst = su32(base + S::kQ + qb * kTB + h * kTile * 128);
-          tma_load_3d(dst, &map_q, 64 * h, w.head * r.group, tok, &q_full[qb]);
-          if (WIDE) tma_load_3d(dst + kTB, &map_q, 64 * h, w.head * r.group, tok + r.tile_tokens, &q_full[qb]);
-        }
-      }
+    for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r)) {
       const int32_t *tab = c.table + int64_t(w.s.slot) * c.max_pages;
       // page of this lane's part of key tile j; c.pages (outside the map: reads as zero) past the keys
       auto page_of = [&](int j) -> int {
@@ -526,9 +521,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int v = 0; v < 2; ++v)
         for (uint32_t i = count[v] > kS ? count[v] - kS : 0; i < count[v]; ++i)
           mbar_wait(&kv_full[v * kS + i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
-      constexpr uint32_t kQBufs = WIDE ? 1 : 2;   // the last fill of each buffer
-      for (uint32_t i = q_issued > kQBufs ? q_issued - kQBufs : 0; i < q_issued; ++i)
-        mbar_wait(&q_full[WIDE ? 0 : i & 1], (WIDE ? i : i >> 1) & 1, &never, kErrDrain, &g_attn_error);
+    }
+    __syncwarp();
+  } else if (warp == kQWarp) {
+    // ------------------------------------------------ copies of Q: a box is a row tile, 64 elements wide
+    if (lane == 0) {
+      constexpr int kHalves = DP / 64, kTiles = WIDE ? 2 : 1;
+      constexpr uint32_t kQBufs = WIDE ? 1 : 2;
+      const uint32_t bytes = uint32_t(r.tile_tokens * r.group) * 128u * kHalves * kTiles;
+      uint32_t items = 0;
+      for (Walk w(c, r, tokens, pl); w.more(); w.next(c, r), ++items) {
+        const uint32_t qb = items % kQBufs, use = items / kQBufs;
+        if (!wait(&q_free[qb], use + 1, kErrQ)) break;
+        mbar_expect_tx(&q_full[qb], bytes);
+        const int tok = w.s.row0 + w.tile * tokens;
+#pragma unroll
+        for (int x = 0; x < kHalves * kTiles; ++x) {
+          const int h = x % kHalves, t = x / kHalves;
+          tma_load_3d(su32(base + S::kQ + (qb + t) * kTB + h * kTile * 128), &map_q, 64 * h, w.head * r.group,
+                      tok + t * r.tile_tokens, &q_full[qb]);
+        }
+      }
+      volatile int never = 0;   // the last fill of each buffer
+      for (uint32_t i = items > kQBufs ? items - kQBufs : 0; i < items; ++i)
+        mbar_wait(&q_full[i % kQBufs], (i / kQBufs) & 1, &never, kErrDrain, &g_attn_error);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -605,6 +621,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t lanes = uint32_t(q4 * 32) << 16;
     const uint32_t t_s = tmem + lanes + st * kTile, t_o = tmem + lanes + 2 * kTile + st * DP;
     const int D = c.head_dim;
+    uint8_t *stage = base + S::kStage + warp * kStageBytes;
     uint32_t tiles = 0, ns = 0, no = 0, nx = 0;   // tiles: key tiles of the pieces before
     bool ok = true;
     for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r)) {
@@ -749,7 +766,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int64_t prow_h = int64_t(prow) * r.q_heads + w.head * r.group + g;
       const int slot = w.t0 == 0 ? 1 : 0;
       const bool whole = w.whole();
-      const int64_t part = int64_t(2 * blockIdx.x + slot) * (WIDE ? 2 * kTile : kTile) + (WIDE ? st * kTile : 0) + row;
+      constexpr int kPartRows = WIDE ? 2 * kTile : kTile;
+      const int part_row = (WIDE ? st * kTile : 0) + row;
+      const int64_t part = int64_t(2 * blockIdx.x + slot) * kPartRows + part_row;
       for (int x0 = 0; x0 < ksteps * 16; x0 += kXCols) {
         float o[kXCols];
         __syncwarp();
@@ -804,19 +823,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
         }
-        if (valid && whole) {
+        if (whole) {
+          // through shared memory, so that a store instruction covers 64 bytes of 8 rows: 16 bytes of 32
+          // rows each would take the L1 32 lines an instruction
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          uint32_t h[kXCols / 2];
-#pragma unroll
-          for (int y = 0; y < kXCols / 2; ++y) h[y] = pack2<T>(o[2 * y] * inv, o[2 * y + 1] * inv);
-          uint4 *dst = reinterpret_cast<uint4 *>(r.out + prow_h * D + x0);
+          uint8_t *sw = stage + lane * (kXCols * 2);
 #pragma unroll
           for (int y = 0; y < kXCols / 8; ++y)
-            if (x0 + 8 * y < D) dst[y] = make_uint4(h[4 * y], h[4 * y + 1], h[4 * y + 2], h[4 * y + 3]);
-        } else if (valid) {
-          float4 *dst = reinterpret_cast<float4 *>(ws.o + part * DP + x0);
+            *reinterpret_cast<uint4 *>(sw + ((y ^ (lane >> 1)) & 3) * 16) =
+                make_uint4(pack2<T>(o[8 * y] * inv, o[8 * y + 1] * inv), pack2<T>(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
+                           pack2<T>(o[8 * y + 4] * inv, o[8 * y + 5] * inv), pack2<T>(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
+          __syncwarp();
 #pragma unroll
-          for (int y = 0; y < kXCols / 4; ++y) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          for (int y = 0; y < 4; ++y) {
+            const int rr = 8 * y + (lane >> 2);
+            const int64_t to = __shfl_sync(0xffffffffu, valid ? prow_h : int64_t(-1), rr);
+            const int col = x0 + 8 * (lane & 3);
+            const uint4 h = *reinterpret_cast<const uint4 *>(stage + rr * (kXCols * 2) + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
+            if (to >= 0 && col < D) *reinterpret_cast<uint4 *>(r.out + to * D + col) = h;
+          }
+          __syncwarp();
+        } else if (valid) {   // columns apart, rows together: a store covers 32 rows of a column
+          float *dst = ws.o + (part - part_row) * DP + int64_t(x0) * kPartRows + part_row;
+#pragma unroll
+          for (int y = 0; y < kXCols; ++y) dst[y * kPartRows] = o[y];
         }
       }
       if (!ok) break;
@@ -829,7 +859,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (!whole && tid == 0) {
         // the item's last unit lies in the share of the last CTA whose first unit is before its end
-        const int64_t end = w.unit - w.t0 + w.total;
+        const int64_t end = w.unit - w.in_item + w.total + kItemCost;
         const int last = int((end * pl.grid + pl.total - 1) / pl.total) - 1;
         Piece p = {1, w.seq, w.tile, w.head, last - int(blockIdx.x) + 1, 0, 0, 0};
         ws.piece[2 * blockIdx.x + slot] = p;
@@ -848,33 +878,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // Join the pieces of the item that CTA blockIdx.x began and did not finish, in the order of the CTAs
-// (so that runs agree).  A thread owns four columns of a row.  grid: (CTAs of the first kernel, rows)
+// (so that runs agree).  A thread owns four columns of a row.  grid: (CTAs of the first kernel, columns)
 template <typename T, int DP, bool WIDE>
 __global__ void __launch_bounds__(256) attn_join_kernel(const KvView c, const Rows r, const Workspace ws) {
   pdl_enter();
   const int cta = blockIdx.x;
   const Piece p = ws.piece[2 * cta + 1];
   if (!p.valid) return;
-  constexpr int kRows = WIDE ? 2 * kTile : kTile, kPer = DP / 4;
+  constexpr int kRows = WIDE ? 2 * kTile : kTile;
   const int tokens = WIDE ? 2 * r.tile_tokens : r.tile_tokens;
   const Seq s = load_seq(c, r, tokens, p.seq);
-  const int x = int(blockIdx.y) * 256 + int(threadIdx.x), row = x / kPer, d = 4 * (x - row * kPer);
+  const int x = int(blockIdx.y) * 256 + int(threadIdx.x), row = x % kRows, d = 4 * (x / kRows);
   const int st = row / kTile, tok_in = (row - st * kTile) / r.group, g = row - st * kTile - tok_in * r.group;
   const int tok = p.tile * tokens + st * r.tile_tokens + tok_in;
-  if (row >= kRows || tok_in >= r.tile_tokens || tok >= s.nq) return;
+  if (tok_in >= r.tile_tokens || tok >= s.nq) return;
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int i = 0; i < p.pieces; ++i) {
-    const int64_t at = int64_t(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * kRows + row;
-    const float2 ml = ws.ml[at];
-    const float4 v = *reinterpret_cast<const float4 *>(ws.o + at * DP + d);
+    const int64_t at = int64_t(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * kRows;
+    const float2 ml = ws.ml[at + row];
+    float v[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) v[y] = ws.o[at * DP + (d + y) * kRows + row];
     if (ml.y == 0.f) continue;
     const float top = fmaxf(m, ml.x), a = m == -INFINITY ? 0.f : ex2(m - top), b = ex2(ml.x - top);
     l = l * a + ml.y * b;
-    o[0] = o[0] * a + v.x * b;
-    o[1] = o[1] * a + v.y * b;
-    o[2] = o[2] * a + v.z * b;
-    o[3] = o[3] * a + v.w * b;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) o[y] = o[y] * a + v[y] * b;
     m = top;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
