@@ -59,8 +59,8 @@ constexpr int kAttnThreads = 32 * 12;      // the third warpgroup: copies, MMA i
 // take over what the third does not need: 2 x 224 + 56 = 3 x 168.
 constexpr int kSoftRegs = 224, kOtherRegs = 56;
 constexpr int kRingBytes = 128 << 10;      // K and V tiles in flight, half of it each
-constexpr int kXCols = 32;                 // columns of the output that the epilogue handles at a time
-constexpr int kStageBytes = 32 * kXCols * 2;   // a softmax warp's 16-bit output rows of those columns
+constexpr int kCols = 32;                  // columns of the output that the epilogue handles at a time
+constexpr int kStageBytes = 32 * kCols * 2;   // a softmax warp's 16-bit output rows of those columns
 // The running maximum is only moved when a tile exceeds it by more than this (in powers of two):
 // weights grow to at most 2^8 of the largest, sums and outputs stay exact in fp32, and the
 // accumulator in tensor memory is hardly ever rescaled.
@@ -306,6 +306,29 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+  float2 y;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %5};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n"
+      " mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+
 // D (tensor memory) (+)= A (tensor memory) x B (shared memory)
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -395,13 +418,13 @@ __device__ __forceinline__ void tc_ld_row(uint32_t taddr, float (&v)[kTile]) {
       : "memory");
 }
 
-// Shared memory of a CTA: Q (two row tiles, or two buffers of one), the ring of K and V tiles, the
-// exchange of the narrow merge, barriers.
+// Shared memory of a CTA: Q (two row tiles, or two buffers of one), the rings of K and V tiles, the
+// streams' maxima and sums for the narrow merge, the softmax warps' output staging, barriers.
 template <int DP> struct Smem {
   static constexpr int kTileBytes = kTile * DP * 2;
   static constexpr int kStages = kRingBytes / kTileBytes / 2;   // of the K ring, and of the V ring
-  static constexpr int kQ = 0, kRing = 2 * kTileBytes, kX = kRing + kRingBytes, kXml = kX + kXCols * kTile * 4,
-                       kStage = kXml + kTile * 8, kBar = kStage + kSoftWarps * kStageBytes, kBars = 2 + 2 + 4 * kStages + 4 * 2 + 2 + 1;
+  static constexpr int kQ = 0, kRing = 2 * kTileBytes, kXml = kRing + kRingBytes, kStage = kXml + 4 * kTile * 8,
+                       kBar = kStage + kSoftWarps * kStageBytes, kBars = 2 + 2 + 4 * kStages + 4 * 2 + 4 + 1;
   static constexpr int kScratch = kBar + kBars * 8, kPlace = kScratch + 32 * 8, kFlags = kPlace + int(sizeof(Place));
   static constexpr int kBytes = kFlags + 16 + 1024 /* alignment */;
 };
@@ -421,12 +444,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr float kShift = kF16 ? 7.f : 0.f;
   extern __shared__ __align__(1024) uint8_t dsmem[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
-  float *xbuf = reinterpret_cast<float *>(base + S::kX);
   float2 *xml = reinterpret_cast<float2 *>(base + S::kXml);
   uint64_t *bar = reinterpret_cast<uint64_t *>(base + S::kBar);
   uint64_t *q_full = bar, *q_free = bar + 2, *kv_full = bar + 4, *kv_free = kv_full + 2 * kS, *s_full = kv_free + 2 * kS,
-           *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *x_full = o_free + 2, *x_free = x_full + 1,
-           *drain = x_free + 1;
+           *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *x_full = o_free + 2,
+           *drain = x_full + 4;
   int64_t *scratch = reinterpret_cast<int64_t *>(base + S::kScratch);
   Place *place = reinterpret_cast<Place *>(base + S::kPlace);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(base + S::kFlags);
@@ -442,14 +464,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 4);
       mbar_init(&o_full[i], 1);
-      mbar_init(&o_free[i], 4);
+      mbar_init(&o_free[i], WIDE ? 4 : 8);
     }
     for (int i = 0; i < 2 * kS; ++i) {   // K stages, then V stages
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_free[i], 1);
     }
-    mbar_init(x_full, 4);
-    mbar_init(x_free, 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&x_full[i], 2);   // the two warps with the same rows
     mbar_init(drain, 1);
     *abort_flag = 0;
     *poison = 0;
@@ -622,7 +643,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t t_s = tmem + lanes + st * kTile, t_o = tmem + lanes + 2 * kTile + st * DP;
     const int D = c.head_dim;
     uint8_t *stage = base + S::kStage + warp * kStageBytes;
-    uint32_t tiles = 0, ns = 0, no = 0, nx = 0;   // tiles: key tiles of the pieces before
+    uint32_t tiles = 0, ns = 0, no[2] = {0, 0}, nx = 0;   // tiles: key tiles of the pieces before
     bool ok = true;
     for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r)) {
       const int n = w.stream_tiles(r, WIDE, st);
@@ -675,8 +696,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-          for (int x = 4; x < kTile; ++x) top[x & 3] = fmaxf(top[x & 3], v[x]);
-          const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * r.scale_log2;
+          for (int x = 4; x < kTile - 4; x += 8) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) top[y] = max3(top[y], v[x + 2 * y], v[x + 2 * y + 1]);
+          }
+          const float mt = max3(max3(top[0], top[1], v[kTile - 1]), max3(top[2], v[kTile - 4], v[kTile - 3]),
+                                fmaxf(top[3], v[kTile - 2])) * r.scale_log2;
           const bool grow = i == 0 ? mt > m : mt > m + kLazy || (m == -INFINITY && mt > m);
           if (i > 0 && __any_sync(0xffffffffu, grow)) {
             // the products that have been added to O are complete: this tile's scores were issued behind them
@@ -692,21 +717,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           if (grow) m = mt;
           const float ref = m == -INFINITY ? 0.f : m - kShift;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t p[16];
 #pragma unroll
             for (int y = 0; y < 16; ++y) {
-              const float a = ex2(fmaf(v[32 * x + 2 * y], r.scale_log2, -ref));
-              const float b = ex2(fmaf(v[32 * x + 2 * y + 1], r.scale_log2, -ref));
-              sum[(2 * y) & 3] += a;
-              sum[(2 * y + 1) & 3] += b;
-              p[y] = pack2<T>(a, b);
+              float2 a = fma2({v[32 * x + 2 * y], v[32 * x + 2 * y + 1]}, r.scale_log2, -ref);
+              a = {ex2(a.x), ex2(a.y)};
+              sum[y & 1] = add2(sum[y & 1], a);
+              p[y] = pack2<T>(a.x, a.y);
             }
             tc_st16(t_s + 16 * x, p);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tc_wait_st();
         }
         if (tile >= edge) {
@@ -747,62 +771,70 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         m = -INFINITY;
         l = 0.f;
       }
-      if (n > 0) {
-        if (!(ok = wait(&o_full[st], no, kErrO))) break;
-        __syncwarp();
-        ++no;
-        tc_fence_after();
-      }
       // the running maximum that goes with l and O as they are
       float ref = m == -INFINITY ? -INFINITY : m - kShift;
-      float mine = 1.f, other = 0.f;   // narrow: factors of the two streams
+      float f[2] = {1.f, 0.f};   // narrow: factors of the two streams' outputs
       const int n1 = WIDE ? 0 : w.cnt >> 1;
-      if (!WIDE && n1 > 0) {
-        if (st == 1) {
-          if (!(ok = wait(x_free, nx + 1, kErrX))) break;
-          xml[row] = make_float2(ref, l);
+      if constexpr (WIDE) {
+        if (n > 0) {
+          if (!(ok = wait(&o_full[st], no[0], kErrO))) break;
+          ++no[0];
+        }
+      } else {
+        // both warps of these rows get the other stream's maximum and sum, and then each merges every
+        // other 32 columns of the two accumulators
+        float2 *mine = xml + (nx & 1) * 2 * kTile + row;
+        mine[st * kTile] = make_float2(ref, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_full[q4]);
+        if (!(ok = wait(&x_full[q4], nx, kErrX))) break;
+        ++nx;
+        const float2 b = mine[(st ^ 1) * kTile];
+        const float top = fmaxf(ref, b.x);
+        f[st] = ref == -INFINITY ? 0.f : ex2(ref - top);
+        f[st ^ 1] = b.x == -INFINITY ? 0.f : ex2(b.x - top);
+        l = st == 0 ? l * f[0] + b.y * f[1] : b.y * f[0] + l * f[1];
+        ref = top;
+        if (!(ok = wait(&o_full[0], no[0], kErrO))) break;
+        ++no[0];
+        if (n1 > 0) {
+          if (!(ok = wait(&o_full[1], no[1], kErrO))) break;
+          ++no[1];
         }
       }
+      __syncwarp();
+      tc_fence_after();
       const int64_t prow_h = int64_t(prow) * r.q_heads + w.head * r.group + g;
       const int slot = w.t0 == 0 ? 1 : 0;
       const bool whole = w.whole();
       constexpr int kPartRows = WIDE ? 2 * kTile : kTile;
       const int part_row = (WIDE ? st * kTile : 0) + row;
-      const int64_t part = int64_t(2 * blockIdx.x + slot) * kPartRows + part_row;
-      for (int x0 = 0; x0 < ksteps * 16; x0 += kXCols) {
-        float o[kXCols];
+      const int64_t part = int64_t(2 * blockIdx.x + slot) * kPartRows;
+      // what this lane stores: 16 bytes at (lane & 3) of rows 8 y + lane / 4, in every 32 columns
+      const uint32_t rows_valid = __ballot_sync(0xffffffffu, valid);
+      uint16_t *to[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        to[y] = r.out + __shfl_sync(0xffffffffu, prow_h, 8 * y + (lane >> 2)) * D + 8 * (lane & 3);
+      for (int x0 = WIDE ? 0 : kCols * st; x0 < ksteps * 16; x0 += WIDE ? kCols : 2 * kCols) {
+        float o[kCols];
         __syncwarp();
-        if (n > 0 && work) tc_ld32(t_o + x0, o);
-        if (n == 0 || l == 0.f) {
+        if (WIDE) {
+          if (n > 0 && work) tc_ld32(t_o + x0, o);
+          if (n == 0 || l == 0.f) {
 #pragma unroll
-          for (int y = 0; y < kXCols; ++y) o[y] = 0.f;
-        }
-        if (!WIDE && n1 > 0) {
-          if (st == 1) {
-            if (x0 > 0 && !(ok = wait(x_free, nx + 1, kErrX))) break;
-#pragma unroll
-            for (int y = 0; y < kXCols; ++y) xbuf[y * kTile + row] = o[y];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(x_full);
-            ++nx;
-            continue;
+            for (int y = 0; y < kCols; ++y) o[y] = 0.f;
           }
-          if (!(ok = wait(x_full, nx, kErrX))) break;
-          ++nx;
-          if (x0 == 0) {
-            const float2 b = xml[row];
-            const float top = fmaxf(ref, b.x);
-            mine = ref == -INFINITY ? 0.f : ex2(ref - top);
-            other = b.x == -INFINITY ? 0.f : ex2(b.x - top);
-            l = l * mine + b.y * other;
-            ref = top;
-          }
+        } else {
+          if (work) tc_ld32(tmem + lanes + 2 * kTile + x0, o);
 #pragma unroll
-          for (int y = 0; y < kXCols; ++y) o[y] = o[y] * mine + xbuf[y * kTile + row] * other;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(x_free);
-        } else if (!WIDE && st == 1) {
-          break;
+          for (int y = 0; y < kCols; ++y) o[y] = f[0] == 0.f ? 0.f : o[y] * f[0];
+          if (n1 > 0 && work) {
+            float o1[kCols];
+            tc_ld32(tmem + lanes + 2 * kTile + DP + x0, o1);
+#pragma unroll
+            for (int y = 0; y < kCols; ++y) o[y] = f[1] == 0.f ? o[y] : fmaf(o1[y], f[1], o[y]);
+          }
         }
         if (valid && *poison && l != 0.f) {
           // new tokens' values that are not finite were taken out of the second product; a row that
@@ -817,7 +849,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const T *vr = reinterpret_cast<const T *>(layer_pool) +
                           ((int64_t(2 * p + 1) * c.kv_heads + w.head) * c.page_size() + (key & (c.page_size() - 1))) * D + x0;
 #pragma unroll
-            for (int y = 0; y < kXCols; ++y) {
+            for (int y = 0; y < kCols; ++y) {
               const float f = x0 + y < D ? to_f32(vr[y]) : 0.f;
               if (!(fabsf(f) < INFINITY)) o[y] += f;
             }
@@ -827,9 +859,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // through shared memory, so that a store instruction covers 64 bytes of 8 rows: 16 bytes of 32
           // rows each would take the L1 32 lines an instruction
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          uint8_t *sw = stage + lane * (kXCols * 2);
+          uint8_t *sw = stage + lane * (kCols * 2);
 #pragma unroll
-          for (int y = 0; y < kXCols / 8; ++y)
+          for (int y = 0; y < kCols / 8; ++y)
             *reinterpret_cast<uint4 *>(sw + ((y ^ (lane >> 1)) & 3) * 16) =
                 make_uint4(pack2<T>(o[8 * y] * inv, o[8 * y + 1] * inv), pack2<T>(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
                            pack2<T>(o[8 * y + 4] * inv, o[8 * y + 5] * inv), pack2<T>(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
@@ -837,24 +869,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int rr = 8 * y + (lane >> 2);
-            const int64_t to = __shfl_sync(0xffffffffu, valid ? prow_h : int64_t(-1), rr);
-            const int col = x0 + 8 * (lane & 3);
-            const uint4 h = *reinterpret_cast<const uint4 *>(stage + rr * (kXCols * 2) + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
-            if (to >= 0 && col < D) *reinterpret_cast<uint4 *>(r.out + to * D + col) = h;
+            if ((rows_valid >> rr & 1u) && x0 + 8 * (lane & 3) < D)
+              *reinterpret_cast<uint4 *>(to[y] + x0) =
+                  *reinterpret_cast<const uint4 *>(stage + rr * (kCols * 2) + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
           }
-          __syncwarp();
         } else if (valid) {   // columns apart, rows together: a store covers 32 rows of a column
-          float *dst = ws.o + (part - part_row) * DP + int64_t(x0) * kPartRows + part_row;
+          float *dst = ws.o + part * DP + int64_t(x0) * kPartRows + part_row;
 #pragma unroll
-          for (int y = 0; y < kXCols; ++y) dst[y * kPartRows] = o[y];
+          for (int y = 0; y < kCols; ++y) dst[y * kPartRows] = o[y];
         }
       }
-      if (!ok) break;
       if (valid && (WIDE || st == 0)) {
         if (whole) {
           if (r.lse) r.lse[prow_h] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
         } else {
-          ws.ml[part] = make_float2(ref, l);
+          ws.ml[part + part_row] = make_float2(ref, l);
         }
       }
       if (!whole && tid == 0) {
@@ -866,7 +895,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (n > 0 && lane == 0) mbar_arrive(&o_free[st]);
+      if (lane == 0) {
+        if (WIDE ? n > 0 : true) mbar_arrive(&o_free[WIDE ? st : 0]);
+        if (!WIDE && n1 > 0) mbar_arrive(&o_free[1]);
+      }
     }
   }
 
