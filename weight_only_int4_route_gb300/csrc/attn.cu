@@ -15,8 +15,8 @@
 //   narrow  one row tile, the streams take alternate key tiles and are merged at the end (few rows
 //           per sequence: memory bound).
 //
-// Work: an item is (sequence, row tile or pair of them, K/V head), its units are kItemCost units of
-// overhead and its key tiles.  The units of all items, in order, are dealt to the CTAs in equal contiguous shares, whatever the lengths
+// Work: an item is (sequence, row tile or pair of them, K/V head), its units are a few units of
+// overhead (kItemCost) and its key tiles.  The units of all items, in order, are dealt to the CTAs in equal contiguous shares, whatever the lengths
 // (which only the device knows); an item cut by a share's boundary leaves partial results (running
 // maximum, sum, unscaled output) in the workspace, and a second kernel joins them in order.
 //
@@ -66,8 +66,9 @@ constexpr int kStageBytes = 32 * kCols * 2;   // a softmax warp's 16-bit output 
 // accumulator in tensor memory is hardly ever rescaled.
 constexpr float kLazy = 8.f;
 // What an item costs beside its key tiles (its queries, its first tiles' latency, its epilogue), in key
-// tiles: shares are dealt with it counted in.
-constexpr int kItemCost = 3;
+// tiles: shares are dealt with it counted in.  Not in calls so small that every key tile gets a CTA
+// of its own (up to kSmallUnits units per CTA): there the longest share decides.
+constexpr int kItemCost = 3, kSmallUnits = 4;
 enum : int { kErrQ = 11, kErrKv = 12, kErrS = 13, kErrP = 14, kErrO = 15, kErrX = 16, kErrDrain = 17 };
 
 struct Rows {
@@ -94,9 +95,25 @@ struct Workspace {
 
 // ---------------------------------------------------------------- work
 
-// sum_{i < n} floor((a i + b) / m), by swapping the roles of the axes as in Euclid's algorithm.
-__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t sum = 0;
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {   // a, b >= 0; the short form where both fit
+  return ((a | b) >> 31) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
+// sum_{i < n} floor((step i + b) / 128).  Steps that divide 128 or are multiples of it (group sizes that are
+// powers of two) have a closed form; else by swapping the roles of the axes as in Euclid's
+// algorithm.
+__device__ int64_t floor_sum(int64_t n, int step, int64_t b) {
+  if (step % kTile == 0) return int64_t(step / kTile) * (n * (n - 1) / 2) + n * (b / kTile);
+  if ((step & (step - 1)) == 0) {   // floor((step i + b) / 128) = floor((i + floor(b / step)) / q), q = 128 / step
+    const int sh = 31 - __clz(kTile / step);
+    auto first = [&](int64_t x) {   // sum_{i < x} floor(i / q)
+      const int64_t a = x >> sh;
+      return ((a * (a - 1)) << sh) / 2 + a * (x - (a << sh));
+    };
+    const int64_t b0 = b >> (31 - __clz(step));
+    return first(b0 + n) - first(b0);
+  }
+  int64_t sum = 0, m = kTile, a = step;
   while (n > 0) {
     if (a >= m) {
       sum += (n - 1) * n / 2 * (a / m);
@@ -148,105 +165,130 @@ __device__ __forceinline__ int64_t key_tiles_before(const Rows &r, const Seq &s,
   if (s.keys == 0) return m;
   if (r.mask) return int64_t(m) * ((s.start + s.nq + kTile - 1) / kTile);
   const int full = min(m, s.tiles - 1);   // the last tile may have fewer tokens
-  int64_t n = floor_sum(full, kTile, tokens, int64_t(s.start) + tokens + kTile - 1);
+  int64_t n = full > 0 ? floor_sum(full, tokens, int64_t(s.start) + tokens + kTile - 1) : 0;
   if (m > full) n += key_tiles(r, s, tokens, s.tiles - 1);
   return n;
 }
 
-__device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t *before, int64_t *scratch /*[32]*/) {
+// Exclusive prefix sums of two values over the block; returns the totals.
+struct Pair64 {
+  int64_t a, b;
+};
+__device__ __forceinline__ Pair64 block_scan_pair(Pair64 v, Pair64 *before, Pair64 *scratch /*[32]*/) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int64_t x = v;
+  Pair64 x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int64_t a = __shfl_up_sync(0xffffffffu, x.a, o), b = __shfl_up_sync(0xffffffffu, x.b, o);
+    if (lane >= o) {
+      x.a += a;
+      x.b += b;
+    }
   }
   if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  int64_t base = 0, total = 0;
+  Pair64 base = {0, 0}, total = {0, 0};
   for (int w = 0; w < nw; ++w) {
-    if (w < warp) base += scratch[w];
-    total += scratch[w];
+    if (w < warp) base = {base.a + scratch[w].a, base.b + scratch[w].b};
+    total = {total.a + scratch[w].a, total.b + scratch[w].b};
   }
   __syncthreads();
-  *before = base + x - v;
+  *before = {base.a + x.a - v.a, base.b + x.b - v.b};
   return total;
 }
 
 // The CTA's place in the work.
 struct Place {
-  int64_t units, total;   // units of this CTA, of all
+  int64_t units, unit0;   // its units, the first of them counted over all
+  int64_t share;          // units per CTA; the first `more` CTAs have one more
+  int more, cost;         // cost: units of overhead per item
   int seq, tile, head, in_item;   // in_item: units of the first item that belong to earlier CTAs
-  int pad;
-  int64_t unit0;          // first unit of this CTA
-  int grid, pad2;         // CTAs with work
+  // the CTA whose share holds unit u
+  __device__ __forceinline__ int owner(int64_t u) const {
+    const int64_t cut = more * (share + 1);
+    return int(u < cut ? div64(u, share + 1) : more + div64(u - cut, share));
+  }
 };
 
 // Every thread of the block calls it; sh is shared.
-__device__ void find_place(const KvView &c, const Rows &r, int tokens, Place *sh, int64_t *scratch) {
+__device__ void find_place(const KvView &c, const Rows &r, int tokens, Place *sh, Pair64 *scratch) {
   const int tid = threadIdx.x, nt = blockDim.x, H = c.kv_heads;
-  auto units = [&](int b) -> int64_t {
-    if (b >= r.n) return 0;
+  auto count = [&](int b) -> Pair64 {   // key tiles and items of sequence b
+    if (b >= r.n) return {0, 0};
     const Seq s = load_seq(c, r, tokens, b);
-    return s.nq > 0 ? H * (key_tiles_before(r, s, tokens, s.tiles) + int64_t(kItemCost) * s.tiles) : 0;
+    return {s.nq > 0 ? H * key_tiles_before(r, s, tokens, s.tiles) : 0, int64_t(H) * s.tiles};
   };
-  int64_t v = 0, before = 0, total = 0;
+  Pair64 v = {0, 0}, before = {0, 0}, total = {0, 0};
   for (int b0 = 0; b0 < r.n; b0 += nt) {
-    v = units(b0 + tid);
-    total += block_scan64(v, &before, scratch);
+    v = count(b0 + tid);
+    const Pair64 sum = block_scan_pair(v, &before, scratch);
+    total = {total.a + sum.a, total.b + sum.b};
   }
-  const int grid = int(min(int64_t(gridDim.x), total));
-  const int cta = blockIdx.x;
-  const int64_t u0 = cta < grid ? total * cta / grid : 0, u1 = cta < grid ? total * (cta + 1) / grid : 0;
+  const int cost = total.a + kItemCost * total.b > int64_t(kSmallUnits) * gridDim.x ? kItemCost : 0;
+  const int64_t units = total.a + cost * total.b, grid = min(int64_t(gridDim.x), max(units, int64_t(1)));
+  const int64_t share = div64(units, grid), cta = blockIdx.x;
+  const int more = int(units - share * grid);
+  const int64_t u0 = share * cta + min(cta, int64_t(more)), mine = cta < grid ? share + (cta < more ? 1 : 0) : 0;
   if (tid == 0) {
-    sh->units = u1 - u0;
-    sh->total = total;
-    sh->grid = grid;
+    sh->units = mine;
     sh->unit0 = u0;
+    sh->share = share;
+    sh->more = more;
+    sh->cost = cost;
   }
-  if (u1 > u0) {
+  if (mine > 0) {
     int64_t base = 0;
     for (int b0 = 0; b0 < r.n; b0 += nt) {
-      int64_t sum = total;
+      Pair64 sum = total;
       if (r.n > nt) {   // one round of threads covers the usual call: its scan is still in registers
-        v = units(b0 + tid);
-        sum = block_scan64(v, &before, scratch);
+        v = count(b0 + tid);
+        sum = block_scan_pair(v, &before, scratch);
       }
-      const int64_t at = base + before;
-      if (u0 >= at && u0 < at + v) {
+      const int64_t at = base + before.a + cost * before.b;
+      if (u0 >= at && u0 < at + v.a + cost * v.b) {
         const int b = b0 + tid;
         const Seq s = load_seq(c, r, tokens, b);
         int64_t off = u0 - at;
+        auto units_before = [&](int m) { return H * (key_tiles_before(r, s, tokens, m) + int64_t(cost) * m); };
         int lo = 0, hi = s.tiles - 1;
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (H * (key_tiles_before(r, s, tokens, mid) + int64_t(kItemCost) * mid) <= off) lo = mid;
+          if (units_before(mid) <= off) lo = mid;
           else hi = mid - 1;
         }
-        off -= H * (key_tiles_before(r, s, tokens, lo) + int64_t(kItemCost) * lo);
-        const int kt = key_tiles(r, s, tokens, lo) + kItemCost;
+        off -= units_before(lo);
+        const int len = key_tiles(r, s, tokens, lo) + cost;
         sh->seq = b;
         sh->tile = lo;
-        sh->head = int(off / kt);
-        sh->in_item = int(off % kt);
+        sh->head = int(div64(off, len));
+        sh->in_item = int(off - int64_t(sh->head) * len);
       }
-      base += sum;
+      base += sum.a + cost * sum.b;
     }
   }
   __syncthreads();
 }
 
-// Walks the pieces of items in the CTA's share; every warp role walks the same way.
+// Walks the pieces of items in the CTA's share; every warp walks the same way.  The walk lives in shared
+// memory, one per warp: a softmax thread needs its registers for a row of scores.
 struct Walk {
   int64_t left, unit;       // units left, first unit of the present piece
   int seq, tile, head;
   int in_item, take;        // the piece: units [in_item, in_item + take) of the item
   int t0, cnt, total;       // its key tiles [t0, t0 + cnt) of the item's total
   Seq s;
-  int n, heads, tokens;
-  __device__ __forceinline__ Walk(const KvView &c, const Rows &r, int tokens_, const Place &p)
-      : left(p.units), unit(p.unit0), seq(p.seq), tile(p.tile), head(p.head), in_item(p.in_item), n(r.n), heads(c.kv_heads),
-        tokens(tokens_) {
+  int n, heads, tokens, cost;
+  __device__ void begin(const KvView &c, const Rows &r, int tokens_, const Place &p) {
+    left = p.units;
+    unit = p.unit0;
+    seq = p.seq;
+    tile = p.tile;
+    head = p.head;
+    in_item = p.in_item;
+    n = r.n;
+    heads = c.kv_heads;
+    tokens = tokens_;
+    cost = p.cost;
     if (left > 0) {
       s = load_seq(c, r, tokens, seq);
       open(r);
@@ -255,13 +297,13 @@ struct Walk {
   }
   __device__ __forceinline__ void open(const Rows &r) {
     total = key_tiles(r, s, tokens, tile);
-    take = int(min(int64_t(total + kItemCost - in_item), left));
-    t0 = max(in_item - kItemCost, 0);
-    cnt = max(in_item + take - kItemCost, 0) - t0;
+    take = int(min(int64_t(total + cost - in_item), left));
+    t0 = max(in_item - cost, 0);
+    cnt = max(in_item + take - cost, 0) - t0;
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && cnt == total; }
-  __device__ __forceinline__ void next(const KvView &c, const Rows &r) {
+  __device__ void next(const KvView &c, const Rows &r) {
     left -= take;
     unit += take;
     if (left <= 0) return;
@@ -375,6 +417,9 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
 }
 constexpr uint32_t kTransposeB = 1u << 16;   // instruction descriptor: B is N-major
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
@@ -424,17 +469,22 @@ template <int DP> struct Smem {
   static constexpr int kTileBytes = kTile * DP * 2;
   static constexpr int kStages = kRingBytes / kTileBytes / 2;   // of the K ring, and of the V ring
   static constexpr int kQ = 0, kRing = 2 * kTileBytes, kXml = kRing + kRingBytes, kStage = kXml + 4 * kTile * 8,
-                       kBar = kStage + kSoftWarps * kStageBytes, kBars = 2 + 2 + 4 * kStages + 4 * 2 + 4 + 1;
-  static constexpr int kScratch = kBar + kBars * 8, kPlace = kScratch + 32 * 8, kFlags = kPlace + int(sizeof(Place));
+                       kScratch = kStage + kSoftWarps * kStageBytes, kBar = kScratch + 32 * 16, kBars = 2 + 2 + 4 * kStages + 4 * 2 + 4 + 1;
+  static constexpr int kPlace = kBar + kBars * 8, kWalks = kPlace + int(sizeof(Place)),
+                       kFlags = kWalks + kAttnThreads / 32 * int(sizeof(Walk));
   static constexpr int kBytes = kFlags + 16 + 1024 /* alignment */;
 };
 static_assert(Smem<128>::kBytes <= 232448 && Smem<64>::kBytes <= 232448, "shared memory");
-static_assert(sizeof(Place) % 8 == 0, "flags follow the place");
+static_assert(sizeof(Place) % 8 == 0 && sizeof(Walk) % 8 == 0, "the flags follow them");
 
 template <typename T, int DP, bool WIDE>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kv, const KvView c,
                 const Rows r, const uint16_t *layer_pool, const Workspace ws) {
+  if (threadIdx.x == 0) {   // the maps are kernel parameters: no need to wait for the kernel before
+    prefetch_map(&map_q);
+    prefetch_map(&map_kv);
+  }
   pdl_enter();
   using S = Smem<DP>;
   constexpr int kS = S::kStages, kTB = S::kTileBytes;
@@ -449,15 +499,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t *q_full = bar, *q_free = bar + 2, *kv_full = bar + 4, *kv_free = kv_full + 2 * kS, *s_full = kv_free + 2 * kS,
            *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *x_full = o_free + 2,
            *drain = x_full + 4;
-  int64_t *scratch = reinterpret_cast<int64_t *>(base + S::kScratch);
+  Pair64 *scratch = reinterpret_cast<Pair64 *>(base + S::kScratch);
   Place *place = reinterpret_cast<Place *>(base + S::kPlace);
+  Walk *walks = reinterpret_cast<Walk *>(base + S::kWalks);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(base + S::kFlags);
   volatile int *poison = abort_flag + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + S::kFlags + 8);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tokens = WIDE ? 2 * r.tile_tokens : r.tile_tokens;   // tokens of an item
-  if (tid == 0) {
+  if (warp == 0) {   // under the latency of the index loads below
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(tmem_slot)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
+  }
+  if (tid == 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_free[i], 1);
@@ -479,17 +534,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     ws.piece[2 * blockIdx.x + 1].valid = 0;
   }
   find_place(c, r, tokens, place, scratch);
-  const Place pl = *place;
-  if (pl.units == 0) return;
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(tmem_slot)), "r"(512u));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
-  }
+  Walk &w = walks[warp];   // find_place ends with a barrier
+  if (lane == 0) w.begin(c, r, tokens, *place);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (place->units == 0) {
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+    return;
+  }
   const int ksteps = (c.head_dim + 15) / 16;   // 16-wide steps of head_dim that hold anything
+  auto next_item = [&] {   // a whole warp's step
+    __syncwarp();
+    if (lane == 0) w.next(c, r);
+    __syncwarp();
+  };
   auto wait = [&](uint64_t *b, uint32_t parity, int code) { return mbar_wait(b, parity & 1, abort_flag, code, &g_attn_error); };
 
   if (warp >= kSoftWarps) {
@@ -500,12 +560,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int halves = DP / 64;
     uint32_t count[2] = {0, 0};
     bool ok = true;
-    for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r)) {
+    for (; ok && w.more(); next_item()) {
+      const int cnt = w.cnt, t0 = w.t0, keys = w.s.keys, head = w.head;
       const int32_t *tab = c.table + int64_t(w.s.slot) * c.max_pages;
       // page of this lane's part of key tile j; c.pages (outside the map: reads as zero) past the keys
       auto page_of = [&](int j) -> int {
-        const int key = (w.t0 + j) * kTile + lane * ps;
-        if (j >= w.cnt || lane >= per || key >= w.s.keys) return c.pages;
+        const int key = (t0 + j) * kTile + lane * ps;
+        if (j >= cnt || lane >= per || key >= keys) return c.pages;
         const int p = __ldg(tab + (key >> c.page_shift));
         if (p >= 0 && p < c.pages) return p;
         if (MOE_CHECKED) check_fail(kCheckPage);
@@ -519,18 +580,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
         if (lane < per) {
           const uint32_t dst = su32(base + S::kRing + s * kTB) + lane * box * 128;
-          const int slot = ((w.t0 + j) * kTile) & (ps - 1);   // nonzero in 256-token pages only
+          const int slot = ((t0 + j) * kTile) & (ps - 1);   // nonzero in 256-token pages only
 #pragma unroll
           for (int h = 0; h < halves; ++h)
-            tma_load_4d(dst + h * kTile * 128, &map_kv, 64 * h, slot, w.head, 2 * page + v, &kv_full[s]);
+            tma_load_4d(dst + h * kTile * 128, &map_kv, 64 * h, slot, head, 2 * page + v, &kv_full[s]);
         }
         return true;
       };
       // in the order of their use: K0 K1 V0 K2 V1 ...
       int p0 = page_of(0), p1 = page_of(1);
       ok = copy(0, p0, 0);
-      for (int j = 0; ok && j < w.cnt; ++j) {
-        if (j + 1 < w.cnt) ok = copy(j + 1, p1, 0);
+      for (int j = 0; ok && j < cnt; ++j) {
+        if (j + 1 < cnt) ok = copy(j + 1, p1, 0);
         const int p2 = page_of(j + 2);
         ok = ok && copy(j, p0, 1);
         p0 = p1;
@@ -551,7 +612,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       constexpr uint32_t kQBufs = WIDE ? 1 : 2;
       const uint32_t bytes = uint32_t(r.tile_tokens * r.group) * 128u * kHalves * kTiles;
       uint32_t items = 0;
-      for (Walk w(c, r, tokens, pl); w.more(); w.next(c, r), ++items) {
+      for (; w.more(); w.next(c, r), ++items) {
         const uint32_t qb = items % kQBufs, use = items / kQBufs;
         if (!wait(&q_free[qb], use + 1, kErrQ)) break;
         mbar_expect_tx(&q_full[qb], bytes);
@@ -580,7 +641,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                      v0_desc = v_desc(su32(base + S::kRing + kS * kTB));
       uint32_t kc = 0, vc = 0, items = 0, np[2] = {0, 0}, no[2] = {0, 0};
       bool ok = true;
-      for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r), ++items) {
+      for (; ok && w.more(); w.next(c, r), ++items) {
         const int qb = WIDE ? 0 : items & 1;
         const int n0 = w.stream_tiles(r, WIDE, 0), n1 = w.stream_tiles(r, WIDE, 1);
         const int events = WIDE ? 2 * w.cnt : w.cnt;
@@ -645,8 +706,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint8_t *stage = base + S::kStage + warp * kStageBytes;
     uint32_t tiles = 0, ns = 0, no[2] = {0, 0}, nx = 0;   // tiles: key tiles of the pieces before
     bool ok = true;
-    for (Walk w(c, r, tokens, pl); ok && w.more(); w.next(c, r)) {
-      const int n = w.stream_tiles(r, WIDE, st);
+    for (; ok && w.more(); next_item()) {
+      const int n = w.stream_tiles(r, WIDE, st), t0 = w.t0, start = w.s.start, keys = w.s.keys;
       const int tok = w.tile * tokens + (WIDE ? st * r.tile_tokens : 0) + tok_in;
       bool live = tok_in < r.tile_tokens && tok < w.s.nq;
       const int prow = w.s.row0 + tok;   // packed row
@@ -659,12 +720,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       const bool work = __any_sync(0xffffffffu, live);
       // causal: keys this row sees; the tiles from `edge` on are not seen whole by every row of the stream
-      const int lim = w.s.keys == 0 ? 0 : (r.mask ? w.s.keys : min(w.s.start + tok + 1, w.s.keys));
-      const int edge = w.s.keys == 0 ? 0
-                       : (r.mask ? w.s.start : min(w.s.start + tok - tok_in + 1, w.s.keys)) / kTile;
+      const int lim = keys == 0 ? 0 : (r.mask ? keys : min(start + tok + 1, keys));
+      const int edge = keys == 0 ? 0
+                       : (r.mask ? start : min(start + tok - tok_in + 1, keys)) / kTile;
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i) {
-        const int j = WIDE ? i : 2 * i + st, tile = w.t0 + j;
+        const int j = WIDE ? i : 2 * i + st, tile = t0 + j;
         if (!(ok = wait(&s_full[st], ns, kErrS))) break;
         __syncwarp();
         ++ns;
@@ -679,7 +740,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const int k0 = key0 + 32 * x, in = min(max(lim - k0, 0), 32);
               uint32_t see = in >= 32 ? 0xffffffffu : (1u << in) - 1u;
               if (r.mask) {
-                const int rel = k0 - w.s.start;   // new token of bit 0
+                const int rel = k0 - start;   // new token of bit 0
                 uint32_t word = 0xffffffffu;
                 if (rel > -32) {
                   const int a = rel >= 0 ? rel >> 5 : -1;
@@ -741,8 +802,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (!(ok = wait(&kv_full[kS + vi % kS], vi / kS, kErrKv))) break;
           uint8_t *vt = base + S::kRing + (kS + vi % kS) * kTB + row * 128;
           const int key = tile * kTile + row;
-          if (key >= w.s.start) {
-            const bool past = key >= w.s.keys;
+          if (key >= start) {
+            const bool past = key >= keys;
             for (int x = 0; x < DP / 8; ++x) {
               uint4 *q = reinterpret_cast<uint4 *>(vt + (x >> 3) * kTile * 128) + ((x ^ row) & 7);
               constexpr uint32_t kExp = kF16 ? 0x7C00u : 0x7F80u;
@@ -836,25 +897,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int y = 0; y < kCols; ++y) o[y] = f[1] == 0.f ? o[y] : fmaf(o1[y], f[1], o[y]);
           }
         }
-        if (valid && *poison && l != 0.f) {
-          // new tokens' values that are not finite were taken out of the second product; a row that
-          // sees one gets it here (whatever its weight, the result is the same infinity or NaN)
-          const int32_t *tab = c.table + int64_t(w.s.slot) * c.max_pages;
-          const int k1 = min(lim, (w.t0 + w.cnt) * kTile);
-          for (int key = max(w.s.start, w.t0 * kTile); key < k1; ++key) {
-            const int a = key - w.s.start;
-            if (bits && !((a >> 5) < r.words && ((__ldg(bits + (a >> 5)) >> (a & 31)) & 1u))) continue;
-            const int p = __ldg(tab + (key >> c.page_shift));
-            if (p < 0 || p >= c.pages) continue;
-            const T *vr = reinterpret_cast<const T *>(layer_pool) +
-                          ((int64_t(2 * p + 1) * c.kv_heads + w.head) * c.page_size() + (key & (c.page_size() - 1))) * D + x0;
-#pragma unroll
-            for (int y = 0; y < kCols; ++y) {
-              const float f = x0 + y < D ? to_f32(vr[y]) : 0.f;
-              if (!(fabsf(f) < INFINITY)) o[y] += f;
-            }
-          }
-        }
         if (whole) {
           // through shared memory, so that a store instruction covers 64 bytes of 8 rows: 16 bytes of 32
           // rows each would take the L1 32 lines an instruction
@@ -879,6 +921,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int y = 0; y < kCols; ++y) dst[y * kPartRows] = o[y];
         }
       }
+      if (*poison) {
+        // new tokens' values that are not finite were taken out of the second product; a row that
+        // sees one gets it here (whatever its weight, the result is the same infinity or NaN)
+        __syncwarp();
+        const int32_t *tab = c.table + int64_t(w.s.slot) * c.max_pages;
+        const int k1 = valid && l != 0.f ? min(lim, (w.t0 + w.cnt) * kTile) : 0;
+        for (int key = max(w.s.start, w.t0 * kTile); key < k1; ++key) {
+          const int a = key - w.s.start;
+          if (bits && !((a >> 5) < r.words && ((__ldg(bits + (a >> 5)) >> (a & 31)) & 1u))) continue;
+          const int p = __ldg(tab + (key >> c.page_shift));
+          if (p < 0 || p >= c.pages) continue;
+          const T *vr = reinterpret_cast<const T *>(layer_pool) +
+                        ((int64_t(2 * p + 1) * c.kv_heads + w.head) * c.page_size() + (key & (c.page_size() - 1))) * D;
+#pragma unroll 1
+          for (int d = 0; d < D; ++d) {
+            const float x = to_f32(vr[d]);
+            if (fabsf(x) < INFINITY || (!WIDE && ((d / kCols) & 1) != st)) continue;
+            if (whole) {
+              T *y = reinterpret_cast<T *>(r.out) + prow_h * D + d;
+              *y = from_f32<T>(to_f32(*y) + x);
+            } else {
+              ws.o[part * DP + int64_t(d) * kPartRows + part_row] += x;
+            }
+          }
+        }
+      }
       if (valid && (WIDE || st == 0)) {
         if (whole) {
           if (r.lse) r.lse[prow_h] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
@@ -887,9 +955,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       if (!whole && tid == 0) {
-        // the item's last unit lies in the share of the last CTA whose first unit is before its end
-        const int64_t end = w.unit - w.in_item + w.total + kItemCost;
-        const int last = int((end * pl.grid + pl.total - 1) / pl.total) - 1;
+        const int last = place->owner(w.unit - w.in_item + w.total + w.cost - 1);   // the item's last unit
         Piece p = {1, w.seq, w.tile, w.head, last - int(blockIdx.x) + 1, 0, 0, 0};
         ws.piece[2 * blockIdx.x + slot] = p;
       }
@@ -924,20 +990,31 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const KvView c, const Ro
   const int st = row / kTile, tok_in = (row - st * kTile) / r.group, g = row - st * kTile - tok_in * r.group;
   const int tok = p.tile * tokens + st * r.tile_tokens + tok_in;
   if (tok_in >= r.tile_tokens || tok >= s.nq) return;
+  // kBatch pieces' loads are in flight together: one after the other their latencies would add up
+  constexpr int kBatch = 8;
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = 0; i < p.pieces; ++i) {
-    const int64_t at = int64_t(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * kRows;
-    const float2 ml = ws.ml[at + row];
-    float v[4];
+  for (int i0 = 0; i0 < p.pieces; i0 += kBatch) {
+    float2 ml[kBatch];
+    float v[kBatch][4];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) v[y] = ws.o[at * DP + (d + y) * kRows + row];
-    if (ml.y == 0.f) continue;
-    const float top = fmaxf(m, ml.x), a = m == -INFINITY ? 0.f : ex2(m - top), b = ex2(ml.x - top);
-    l = l * a + ml.y * b;
+    for (int i = 0; i < kBatch; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (i0 + i < p.pieces) {
+        const int64_t at = int64_t(i0 + i == 0 ? 2 * cta + 1 : 2 * (cta + i0 + i)) * kRows;
+        ml[i] = ws.ml[at + row];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) o[y] = o[y] * a + v[y] * b;
-    m = top;
+        for (int y = 0; y < 4; ++y) v[i][y] = ws.o[at * DP + (d + y) * kRows + row];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (ml[i].y == 0.f) continue;
+      const float top = fmaxf(m, ml[i].x), a = m == -INFINITY ? 0.f : ex2(m - top), b = ex2(ml[i].x - top);
+      l = l * a + ml[i].y * b;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) o[y] = o[y] * a + v[i][y] * b;
+      m = top;
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t at = int64_t(s.row0 + tok) * r.q_heads + p.head * r.group + g;
