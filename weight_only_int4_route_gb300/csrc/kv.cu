@@ -4,6 +4,8 @@
 // The free pages are those nobody holds (refs == 0) and allocation takes the lowest-numbered ones in
 // the order (sequence of the call, place in the sequence): no free list whose order would depend on
 // the order of atomic pushes, so every result is the same on every run and any launch shape.
+#include <type_traits>
+
 #include "kv_internal.cuh"
 
 namespace moe {
@@ -117,12 +119,20 @@ __global__ void __launch_bounds__(kBook) kv_extend_kernel(const KvView c, const 
   __syncthreads();
   int found = 0;
   if (fits && total <= c.pages) {
-    for (int p0 = 0; p0 < c.pages && found < total; p0 += kBook) {
-      const int p = p0 + tid;
-      const int is_free = p < c.pages && c.refs[p] == 0;
+    for (int p0 = 0; p0 < c.pages && found < total; p0 += 4 * kBook) {
+      const int p = p0 + 4 * tid;
+      int4 held = make_int4(1, 1, 1, 1);
+      if (p + 3 < c.pages) held = *reinterpret_cast<const int4 *>(c.refs + p);
+      else if (p < c.pages) held = make_int4(c.refs[p], p + 1 < c.pages ? c.refs[p + 1] : 1, p + 2 < c.pages ? c.refs[p + 2] : 1, 1);
+      const int free4[4] = {held.x == 0, held.y == 0, held.z == 0, held.w == 0};
       int at = 0;
-      const int sum = block_exclusive_scan(is_free, &at, scratch);
-      if (is_free && found + at < total) w.page[found + at] = p;
+      const int sum = block_exclusive_scan(free4[0] + free4[1] + free4[2] + free4[3], &at, scratch);
+      at += found;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if (free4[y] && at < total) w.page[at] = p + y;
+        at += free4[y];
+      }
       found += sum;
     }
   }
@@ -220,50 +230,88 @@ __device__ __forceinline__ Kept kept(const KvView &c, const int32_t *seqs, const
   return k;
 }
 
-// Moves.  A thread owns one 16-byte piece of a row (of one layer, K or V, head) and walks the kept
-// tokens in order: entry j is read at offset keep[j] >= j and written at offset j, and no later entry
-// reads an offset already written (ascending: keep[j'] >= j' > j).  grid: (pieces, layers, sequences)
-__global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvView c, const int32_t *__restrict__ seqs,
-                                                              const int32_t *__restrict__ start,
-                                                              const int32_t *__restrict__ cu_keep,
-                                                              const int32_t *__restrict__ keep, int64_t keep_len, int n) {
-  pdl_enter();
-  const int dv = c.head_dim / 8, rows = 2 * c.kv_heads;
-  for (int i = blockIdx.z; i < n; i += gridDim.z) {
-    const Kept k = kept(c, seqs, start, cu_keep, keep_len, i);
-    if (k.slot < 0 || k.count == 0) continue;
-    const int32_t *tab = c.table + int64_t(k.slot) * c.max_pages;
-    uint16_t *layer = c.pool + int64_t(blockIdx.y) * c.layer_elems();
-    for (int e = blockIdx.x * kThreads + threadIdx.x; e < rows * dv; e += gridDim.x * kThreads) {
-      const int row = e / dv, piece = e - row * dv;   // row = (K or V) * kv_heads + head
-      auto at = [&](int pos) -> uint4 * {
-        const int p = valid_page(c, tab[pos >> c.page_shift]);
-        if (p < 0) return nullptr;
-        const int64_t slot = (int64_t(p) * rows + row) * c.page_size() + (pos & (c.page_size() - 1));
-        return reinterpret_cast<uint4 *>(layer + slot * c.head_dim) + piece;
-      };
-      for (int j = 0; j < k.count; ++j) {
-        const int from = keep[k.k0 + j];
-        if (from <= j || from >= k.len - k.start) continue;
-        uint4 *s = at(k.start + from), *d = at(k.start + j);
-        if (s && d) *d = *s;
+// Moves of sequence k on one layer.  A thread owns one 16-byte piece of a row (K or V, head) and walks
+// the kept tokens in order: entry j is read at offset keep[j] >= j and written at offset j, and no later
+// entry reads an offset already written (ascending: keep[j'] >= j' > j); so a batch may be read before
+// it is written.  from / to: where the batch's tokens lie in a layer, worked out once for the block.
+constexpr int kMoves = 128, kMoveBatch = 8;
+struct MoveTable {
+  int64_t from[kMoves], to[kMoves];   // element offset of the token's slot in K of head 0, -1: nothing to move
+};
+__device__ void move_tokens(const KvView &c, const Kept &k, const int32_t *__restrict__ keep, MoveTable *mt, int layer0,
+                            int layers, int piece0, int stride) {
+  const int dv = c.head_dim / 8, pieces = 2 * c.kv_heads * dv, ps = c.page_size();
+  const int32_t *tab = c.table + int64_t(k.slot) * c.max_pages;
+  for (int j0 = 0; j0 < k.count; j0 += kMoves) {
+    const int n = min(kMoves, k.count - j0);
+    __syncthreads();   // the table before has been used
+    for (int j = threadIdx.x; j < kMoves; j += blockDim.x) {
+      int64_t f = -1, t = -1;
+      if (j < n) {
+        const int from = keep[k.k0 + j0 + j];
+        if (from > j0 + j && from < k.len - k.start) {
+          auto at = [&](int pos) -> int64_t {
+            const int p = valid_page(c, tab[pos >> c.page_shift]);
+            return p < 0 ? -1 : (int64_t(p) * 2 * c.kv_heads * ps + (pos & (ps - 1))) * c.head_dim;
+          };
+          f = at(k.start + from);
+          t = at(k.start + j0 + j);
+          if (f < 0 || t < 0) f = t = -1;
+        }
+      }
+      mt->from[j] = f;
+      mt->to[j] = t;
+    }
+    __syncthreads();
+    for (int e = piece0; e < pieces * layers; e += stride) {
+      const int layer = e / pieces, x = e - layer * pieces, row = x / dv;
+      uint16_t *base = c.pool + int64_t(layer0 + layer) * c.layer_elems() + int64_t(row) * ps * c.head_dim + (x - row * dv) * 8;
+      for (int j = 0; j < n; j += kMoveBatch) {
+        uint4 v[kMoveBatch];
+#pragma unroll
+        for (int y = 0; y < kMoveBatch; ++y)   // n <= kMoves, a multiple of the batch: entries past n are -1
+          if (mt->from[j + y] >= 0) v[y] = *reinterpret_cast<const uint4 *>(base + mt->from[j + y]);
+#pragma unroll
+        for (int y = 0; y < kMoveBatch; ++y)
+          if (mt->from[j + y] >= 0) *reinterpret_cast<uint4 *>(base + mt->to[j + y]) = v[y];
       }
     }
   }
 }
 
-// Lengths and pages after the moves.  One block per sequence.
-__global__ void __launch_bounds__(kThreads) kv_shrink_kernel(const KvView c, const int32_t *__restrict__ seqs,
-                                                             const int32_t *__restrict__ start,
-                                                             const int32_t *__restrict__ cu_keep, int64_t keep_len) {
-  pdl_enter();
-  const Kept k = kept(c, seqs, start, cu_keep, keep_len, blockIdx.x);
-  __syncthreads();   // every thread has read the length
-  if (k.slot < 0) return;
+__device__ __forceinline__ void shrink(const KvView &c, const Kept &k) {
   const int len = k.start + k.count;
-  for (int i = pages_for(c, len) + threadIdx.x; i < pages_for(c, k.len); i += kThreads)
+  for (int i = pages_for(c, len) + threadIdx.x; i < pages_for(c, k.len); i += blockDim.x)
     release(c, atomicExch(&c.table[int64_t(k.slot) * c.max_pages + i], -1));
   if (threadIdx.x == 0) c.lens[k.slot] = len;
+}
+
+// grid: (pieces, layers, sequences)
+__global__ void __launch_bounds__(kThreads) kv_move_kernel(const KvView c, const int32_t *__restrict__ seqs,
+                                                           const int32_t *__restrict__ start,
+                                                           const int32_t *__restrict__ cu_keep,
+                                                           const int32_t *__restrict__ keep, int64_t keep_len, int n) {
+  pdl_enter();
+  __shared__ MoveTable mt;
+  for (int i = blockIdx.z; i < n; i += gridDim.z) {
+    const Kept k = kept(c, seqs, start, cu_keep, keep_len, i);
+    if (k.slot >= 0)
+      move_tokens(c, k, keep, &mt, int(blockIdx.y), 1, int(blockIdx.x * kThreads + threadIdx.x), int(gridDim.x * kThreads));
+  }
+}
+
+// Lengths and pages, after the moves; in small caches (kMoveInside) the moves too.  One block per sequence.
+__global__ void __launch_bounds__(kThreads) kv_shrink_kernel(const KvView c, const int32_t *__restrict__ seqs,
+                                                             const int32_t *__restrict__ start,
+                                                             const int32_t *__restrict__ cu_keep,
+                                                             const int32_t *__restrict__ keep, int64_t keep_len, int move) {
+  pdl_enter();
+  __shared__ MoveTable mt;
+  const Kept k = kept(c, seqs, start, cu_keep, keep_len, blockIdx.x);
+  if (k.slot < 0) return;
+  if (move) move_tokens(c, k, keep, &mt, 0, c.layers, int(threadIdx.x), kThreads);
+  __syncthreads();   // every thread has read the length and the table
+  shrink(c, k);
 }
 
 struct Rows {
@@ -276,49 +324,68 @@ struct Rows {
   int64_t n_pos;
 };
 
-// One thread per element of K, V (and q).  grid: (elements, layers)
-template <typename T>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const Rows r) {
+// A thread owns one unit (see rope.cu) of kItems of a token's 2 kv_heads + q_heads heads on one layer.  Where the
+// token goes (its sequence, slot and page) is worked out once per block and token, under the latency of the
+// data's loads.  grid: (units, layers).
+template <typename T, int V, int kItems>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const Rows r, int units, int turned) {
   pdl_enter();
-  const int D = c.head_dim, H = c.kv_heads, rows = 2 * H + r.q_heads;
-  const int64_t total = int64_t(r.T) * rows * D;
-  const T *k = reinterpret_cast<const T *>(r.k) + int64_t(blockIdx.y) * r.kl;
-  const T *v = reinterpret_cast<const T *>(r.v) + int64_t(blockIdx.y) * r.vl;
-  const T *q = reinterpret_cast<const T *>(r.q);
-  T *pool = reinterpret_cast<T *>(c.pool) + int64_t(r.layer + int(blockIdx.y)) * c.layer_elems();
-  for (int64_t e = int64_t(blockIdx.x) * kThreads + threadIdx.x; e < total; e += int64_t(gridDim.x) * kThreads) {
-    const int d = int(e % D), h = int((e / D) % rows), t = int(e / D / rows);
-    const bool is_q = h >= 2 * H, is_v = !is_q && h >= H;
-    const T *src = is_q ? q + t * r.qt + int64_t(h - 2 * H) * D : (is_v ? v + t * r.vt + int64_t(h - H) * D : k + t * r.kt + int64_t(h) * D);
-    T out = src[d];
-    if (r.cos_sin && !is_v && d < r.rot) {
-      const int half = r.rot / 2;
-      const int i = r.inter ? d / 2 : (d < half ? d : d - half);
-      const bool second = r.inter ? (d & 1) != 0 : d >= half;
-      const int p = r.pos[t];
-      float cs = NAN, sn = NAN;
-      if (p >= 0 && p < r.n_pos) {
-        cs = r.cos_sin[int64_t(p) * r.rot + i];
-        sn = r.cos_sin[int64_t(p) * r.rot + half + i];
-      } else if (MOE_CHECKED) {
-        check_fail(kCheckPos);
+  __shared__ int64_t slot_of[kThreads + 1];   // element offset in a layer of K of head 0, -1: not written
+  const int D = c.head_dim, H = c.kv_heads, heads = 2 * H + r.q_heads;
+  const unsigned groups = unsigned(heads + kItems - 1) / kItems, per = groups * unsigned(units);
+  auto token = [&](int64_t x) { return (x >> 32) == 0 ? int64_t(unsigned(x) / per) : x / per; };
+  const int64_t x0 = int64_t(blockIdx.x) * kThreads, x = x0 + threadIdx.x, t0 = token(x0), t = token(x);
+  const unsigned in = unsigned(x - t * per), group = in / unsigned(units);
+  const int unit = int(in - group * unsigned(units)), h0 = int(group) * kItems;
+  const bool have = t < r.T;
+  RopeUnit<T, V> u[kItems];
+  const int layer = int(blockIdx.y);
+  if (have) {
+    const T *k = reinterpret_cast<const T *>(r.k) + layer * r.kl + t * r.kt;
+    const T *v = reinterpret_cast<const T *>(r.v) + layer * r.vl + t * r.vt;
+    const T *q = reinterpret_cast<const T *>(r.q) + t * r.qt;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int h = h0 + i;
+      if (h < heads)
+        u[i].load(h < H ? k + int64_t(h) * D : (h < 2 * H ? v + int64_t(h - H) * D : q + int64_t(h - 2 * H) * D), unit, turned,
+                  r.rot, r.inter);
+    }
+  }
+  Angles<V> g;
+  if (have && unit < turned && r.cos_sin)
+    load_angles<V>(g, r.cos_sin, r.n_pos, __ldg(r.pos + t), r.rot, r.inter, unit, 0, [] {
+      if (MOE_CHECKED) check_fail(kCheckPos);
+    });
+  const int64_t tk = t0 + threadIdx.x;   // the block's tokens
+  if (tk <= token(x0 + kThreads - 1) && tk < r.T) {
+    int64_t slot = -1;
+    const int b = seq_of_row(r.cu, r.n, int(tk));
+    if (b >= 0) {
+      const int s = __ldg(r.seqs + b), st = __ldg(r.start + b);
+      const int64_t at = int64_t(st) + tk - __ldg(r.cu + b);
+      if (s >= 0 && s < c.slots && st >= 0 && (at >> c.page_shift) < c.max_pages) {
+        const int p = valid_page(c, c.table[int64_t(s) * c.max_pages + (at >> c.page_shift)]);
+        if (p >= 0) slot = (int64_t(p) * 2 * H * c.page_size() + (at & (c.page_size() - 1))) * D;
       }
-      const float a = to_f32(src[r.inter ? 2 * i : i]), b = to_f32(src[r.inter ? 2 * i + 1 : i + half]);
-      out = from_f32<T>(second ? a * sn + b * cs : a * cs - b * sn);
     }
-    if (is_q) {
-      reinterpret_cast<T *>(r.q_out)[(int64_t(t) * r.q_heads + (h - 2 * H)) * D + d] = out;
-      continue;
+    slot_of[threadIdx.x] = slot;
+  }
+  __syncthreads();
+  if (!have) return;
+  const int64_t slot = slot_of[t - t0];
+  T *pool = reinterpret_cast<T *>(c.pool) + int64_t(r.layer + layer) * c.layer_elems() + slot;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int h = h0 + i;
+    if (h >= 2 * H) {
+      if (h < heads)
+        u[i].store(reinterpret_cast<T *>(r.q_out) + (t * r.q_heads + (h - 2 * H)) * D, unit, turned, r.rot, r.inter, g);
+    } else if (slot >= 0) {
+      T *dst = pool + int64_t(h) * c.page_size() * D;
+      if (h < H) u[i].store(dst, unit, turned, r.rot, r.inter, g);
+      else u[i].copy(dst, unit, turned, r.rot, r.inter);
     }
-    const int b = seq_of_row(r.cu, r.n, t);
-    if (b < 0) continue;
-    const int slot = r.seqs[b], st = r.start[b];
-    if (slot < 0 || slot >= c.slots || st < 0) continue;
-    const int64_t at = int64_t(st) + t - r.cu[b];
-    if ((at >> c.page_shift) >= c.max_pages) continue;
-    const int p = valid_page(c, c.table[int64_t(slot) * c.max_pages + (at >> c.page_shift)]);
-    if (p < 0) continue;
-    pool[((int64_t(p) * 2 * H + h) * c.page_size() + (at & (c.page_size() - 1))) * D + d] = out;
   }
 }
 
@@ -397,13 +464,18 @@ extern "C" int moe_kv_compact(const moe_kv_desc *desc, const moe_kv *kv, const i
   MOE_REQUIRE(aligned16(cu_keep) && aligned16(keep), "pointers must be 16-byte aligned");
   const KvView c = kv_view(desc, kv);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (keep_len > 0) {
-    const dim3 grid(clamp_grid(cdiv(int64_t(2) * c.kv_heads * (c.head_dim / 8), kThreads), 1024), unsigned(c.layers),
-                    clamp_grid(n, 65535));
-    launch_pdl(kv_compact_kernel, grid, dim3(kThreads), 0, st, c, seqs, start, cu_keep, keep, keep_len, int(n));
+  // One launch where a sequence's rows of all layers are few enough for a block (up to kMoveInside pieces of 16 bytes
+  // per token): the second launch costs more than the lost parallelism.
+  constexpr int64_t kMoveInside = 2048;
+  const int64_t pieces = int64_t(2) * c.kv_heads * (c.head_dim / 8);
+  const bool inside = pieces * c.layers <= kMoveInside;
+  if (keep_len > 0 && !inside) {
+    const dim3 grid(clamp_grid(cdiv(pieces, kThreads), 1024), unsigned(c.layers), clamp_grid(n, 65535));
+    launch_pdl(kv_move_kernel, grid, dim3(kThreads), 0, st, c, seqs, start, cu_keep, keep, keep_len, int(n));
     MOE_TRY(check_launch("kv_compact"));
   }
-  launch_pdl(kv_shrink_kernel, dim3(unsigned(n)), dim3(kThreads), 0, st, c, seqs, start, cu_keep, keep_len);
+  launch_pdl(kv_shrink_kernel, dim3(unsigned(n)), dim3(kThreads), 0, st, c, seqs, start, cu_keep, keep, keep_len,
+             int(inside && keep_len > 0));
   return check_launch("kv_compact: pages");
 }
 
@@ -465,14 +537,36 @@ extern "C" int moe_kv_append(const moe_kv_desc *desc, const moe_kv *kv, int64_t 
   a.n = int(r.n);
   a.T = int(r.T);
   a.q_heads = r.q ? int(r.q_heads) : 0;
-  a.rot = int(r.rot);
-  a.inter = r.interleaved;
+  a.rot = r.cos_sin ? int(r.rot) : 0;
+  a.inter = r.interleaved ? 1 : 0;
   a.layer = int(layer);
   a.n_pos = r.n_pos;
-  const int64_t total = r.T * (2 * desc->kv_heads + a.q_heads) * desc->head_dim;
-  const dim3 grid(clamp_grid(cdiv(total, kThreads), int64_t(num_sms()) * 16), unsigned(n_layers));
+  // without rotation every vector is a copy
+  const int V = r.cos_sin ? rope_vec(2, r.rot, r.interleaved) : 8;
+  const int units = rope_units(V, int(desc->head_dim), int(a.rot), a.inter);
+  const int turned = int((a.inter ? a.rot : a.rot / 2) / V);
+  const int64_t heads = 2 * desc->kv_heads + a.q_heads;
+  // several rows a thread in large calls, as in moe_rope
+  const int items = a.inter || turned == 0 ? 8 : 4;
+  const bool many = r.T * heads * units * n_layers >= int64_t(num_sms()) * 1024 * items;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (desc->dtype == MOE_F16) launch_pdl(kv_append_kernel<__half>, grid, dim3(kThreads), 0, st, c, a);
-  else launch_pdl(kv_append_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, c, a);
+  auto go = [&](auto zero, auto vec, auto per) -> int {
+    const int64_t blocks = cdiv(r.T * cdiv(heads, int64_t(decltype(per)::value)) * units, kThreads);
+    MOE_SUPPORT(blocks < (int64_t(1) << 31), "T * heads too large");
+    launch_pdl(kv_append_kernel<decltype(zero), decltype(vec)::value, decltype(per)::value>, dim3(unsigned(blocks), unsigned(n_layers)),
+               dim3(kThreads), 0, st, c, a, units, turned);
+    return MOE_OK;
+  };
+  auto with_heads = [&](auto zero, auto vec) {
+    if (!many) return go(zero, vec, std::integral_constant<int, 1>());
+    return items == 8 ? go(zero, vec, std::integral_constant<int, 8>()) : go(zero, vec, std::integral_constant<int, 4>());
+  };
+  auto with_vec = [&](auto zero) -> int {
+    if (V == 8) return with_heads(zero, std::integral_constant<int, 8>());
+    if (V == 4) return with_heads(zero, std::integral_constant<int, 4>());
+    if (V == 2) return with_heads(zero, std::integral_constant<int, 2>());
+    return with_heads(zero, std::integral_constant<int, 1>());
+  };
+  MOE_TRY(desc->dtype == MOE_F16 ? with_vec(__half{}) : with_vec(__nv_bfloat16{}));
   return check_launch("kv_append");
 }

@@ -57,4 +57,122 @@ __device__ __forceinline__ int seq_of_row(const int32_t *__restrict__ cu, int n,
   return lo;
 }
 
+// ---- rotation of heads in vectors of V elements (16 bytes where the sizes allow)
+
+// Moved as one word of its size (an array of 16-bit values would be moved value by value).
+template <int BYTES> struct Word;
+template <> struct Word<16> { using type = uint4; };
+template <> struct Word<8> { using type = uint2; };
+template <> struct Word<4> { using type = uint32_t; };
+template <> struct Word<2> { using type = uint16_t; };
+template <typename T, int V> struct Pack {
+  using W = typename Word<int(sizeof(T)) * V>::type;
+  W w;
+  __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const W *>(p); }
+  __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<W *>(p) = w; }
+  __device__ __forceinline__ float get(int i) const { return to_f32(reinterpret_cast<const T *>(&w)[i]); }
+  __device__ __forceinline__ void set(int i, float x) { reinterpret_cast<T *>(&w)[i] = from_f32<T>(x); }
+};
+
+// Largest vector, in elements, that divides what has to be divided: half-layout pairs lie rot / 2 apart, interleaved
+// ones side by side; head_dim is a multiple of 8.
+inline int rope_vec(int elem_bytes, int64_t rot, int interleaved) {
+  const int64_t unit = interleaved ? rot : rot / 2;
+  int v = 16 / elem_bytes;
+  while (v > 1 && unit % v != 0) v /= 2;
+  return v;   // interleaved: rot is even, so at least 2
+}
+
+// Units of a head: its rotated vectors (pairs of vectors in the half layout), then the vectors that are copied.
+__host__ __device__ inline int rope_units(int V, int head_dim, int rot, int inter) {
+  return (inter ? rot : rot / 2) / V + (head_dim - rot) / V;
+}
+
+// The cosines and sines of one unit: V of each (half layout) or V / 2 (interleaved).  NaN for positions outside
+// the table.
+template <int V> struct Angles {
+  float c[V], s[V];
+};
+template <int V, typename Bad>
+__device__ __forceinline__ void load_angles(Angles<V> &a, const float *cos_sin, int64_t n_pos, int p, int rot, int inter,
+                                            int unit, int inverse, Bad bad) {
+  const int n = inter ? V / 2 : V;
+  const bool inside = p >= 0 && p < n_pos;
+  if (!inside) bad();
+  const float *row = cos_sin + int64_t(inside ? p : 0) * rot + unit * n;
+  // rows start at multiples of rot, even: pairs are read together where rot / 2 is even too
+  if (V >= 4 && (rot & 3) == 0) {
+#pragma unroll
+    for (int i = 0; i + 1 < V; i += 2)
+      if (i < n) {
+        const float2 c = __ldg(reinterpret_cast<const float2 *>(row + i));
+        const float2 s = __ldg(reinterpret_cast<const float2 *>(row + rot / 2 + i));
+        a.c[i] = c.x;
+        a.c[i + 1] = c.y;
+        a.s[i] = s.x;
+        a.s[i + 1] = s.y;
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) {
+        a.c[i] = __ldg(row + i);
+        a.s[i] = __ldg(row + rot / 2 + i);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < n) {
+      a.c[i] = inside ? a.c[i] : NAN;
+      a.s[i] = inside ? (inverse ? -a.s[i] : a.s[i]) : NAN;
+    }
+}
+
+// One unit: (a, b) -> (a c - b s, a s + b c) in fp32, one rounding; units past the rotated ones are copied.
+template <typename T, int V> struct RopeUnit {
+  Pack<T, V> a, b;
+  __device__ __forceinline__ void load(const T *src, int unit, int turned, int rot, int inter) {
+    if (unit < turned) {
+      a.load(src + unit * V);
+      if (!inter) b.load(src + rot / 2 + unit * V);
+    } else {
+      a.load(src + rot + (unit - turned) * V);
+    }
+  }
+  __device__ __forceinline__ void copy(T *dst, int unit, int turned, int rot, int inter) const {   // the unit as it is
+    if (unit >= turned) {
+      a.store(dst + rot + (unit - turned) * V);
+    } else {
+      a.store(dst + unit * V);
+      if (!inter) b.store(dst + rot / 2 + unit * V);
+    }
+  }
+  __device__ __forceinline__ void store(T *dst, int unit, int turned, int rot, int inter, const Angles<V> &g) const {
+    if (unit >= turned) {
+      a.store(dst + rot + (unit - turned) * V);
+    } else if (inter) {
+      if constexpr (V > 1) {
+        Pack<T, V> y;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          const float x0 = a.get(2 * i), x1 = a.get(2 * i + 1);
+          y.set(2 * i, x0 * g.c[i] - x1 * g.s[i]);
+          y.set(2 * i + 1, x0 * g.s[i] + x1 * g.c[i]);
+        }
+        y.store(dst + unit * V);
+      }
+    } else {
+      Pack<T, V> y, z;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float x0 = a.get(i), x1 = b.get(i);
+        y.set(i, x0 * g.c[i] - x1 * g.s[i]);
+        z.set(i, x0 * g.s[i] + x1 * g.c[i]);
+      }
+      y.store(dst + unit * V);
+      z.store(dst + rot / 2 + unit * V);
+    }
+  }
+};
+
 }  // namespace moe
