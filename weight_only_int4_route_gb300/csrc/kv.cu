@@ -4,8 +4,6 @@
 // The free pages are those nobody holds (refs == 0) and allocation takes the lowest-numbered ones in
 // the order (sequence of the call, place in the sequence): no free list whose order would depend on
 // the order of atomic pushes, so every result is the same on every run and any launch shape.
-#include <type_traits>
-
 #include "kv_internal.cuh"
 
 namespace moe {
@@ -99,12 +97,22 @@ __global__ void __launch_bounds__(kBook) kv_extend_kernel(const KvView c, const 
   const int tid = threadIdx.x;
   if (tid == 0) fits = 1;
   __syncthreads();
+  // the first holders' counts are on their way while the needs are worked out; the first round of sequences stays
+  // in registers (the usual call has no other)
+  auto held4 = [&](int p) -> int4 {
+    if (p + 3 < c.pages) return *reinterpret_cast<const int4 *>(c.refs + p);
+    if (p >= c.pages) return make_int4(1, 1, 1, 1);
+    return make_int4(c.refs[p], p + 1 < c.pages ? c.refs[p + 1] : 1, p + 2 < c.pages ? c.refs[p + 2] : 1, 1);
+  };
+  int4 held = held4(4 * tid);
+  const Growth mine = tid < n ? growth(c, seqs, n_new, tid) : Growth{-1, 0, 0, 0, -1};
+  auto growth_of = [&](int i) { return i == tid ? mine : growth(c, seqs, n_new, i); };
   int total = 0;
   for (int i0 = 0; i0 < n; i0 += kBook) {
     const int i = i0 + tid;
     int need = 0, at = 0;
     if (i < n) {
-      const Growth g = growth(c, seqs, n_new, i);
+      const Growth g = growth_of(i);
       if (g.slot >= 0) {
         if (g.want > c.max_pages) fits = 0;
         else need = max(0, g.want - g.first);
@@ -121,9 +129,7 @@ __global__ void __launch_bounds__(kBook) kv_extend_kernel(const KvView c, const 
   if (fits && total <= c.pages) {
     for (int p0 = 0; p0 < c.pages && found < total; p0 += 4 * kBook) {
       const int p = p0 + 4 * tid;
-      int4 held = make_int4(1, 1, 1, 1);
-      if (p + 3 < c.pages) held = *reinterpret_cast<const int4 *>(c.refs + p);
-      else if (p < c.pages) held = make_int4(c.refs[p], p + 1 < c.pages ? c.refs[p + 1] : 1, p + 2 < c.pages ? c.refs[p + 2] : 1, 1);
+      if (p0 > 0) held = held4(p);
       const int free4[4] = {held.x == 0, held.y == 0, held.z == 0, held.w == 0};
       int at = 0;
       const int sum = block_exclusive_scan(free4[0] + free4[1] + free4[2] + free4[3], &at, scratch);
@@ -140,7 +146,7 @@ __global__ void __launch_bounds__(kBook) kv_extend_kernel(const KvView c, const 
   const bool ok = fits && total <= c.pages && found >= total;
   // decisions first (they read lens, table and refs), then the changes
   for (int i = tid; i < n; i += kBook) {
-    const Growth g = growth(c, seqs, n_new, i);
+    const Growth g = growth_of(i);
     start[i] = ok && g.slot >= 0 ? g.old : -1;
     const bool copy = ok && g.shared >= 0;
     w.cow[2 * i] = copy ? g.shared : -1;
@@ -162,27 +168,49 @@ __global__ void __launch_bounds__(kBook) kv_extend_kernel(const KvView c, const 
   }
 }
 
-// Page src -> page dst on every layer.  grid: (pieces of a page, layers, pairs)
-__device__ __forceinline__ void copy_page(const KvView &c, int src, int dst) {
-  const int64_t per = 2 * c.half_elems() / 8;   // 16-byte vectors of a page
-  const uint4 *s = reinterpret_cast<const uint4 *>(c.pool + int64_t(blockIdx.y) * c.layer_elems()) + src * per;
-  uint4 *d = reinterpret_cast<uint4 *>(c.pool + int64_t(blockIdx.y) * c.layer_elems()) + dst * per;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < per; i += int64_t(gridDim.x) * blockDim.x) d[i] = s[i];
+// Page copies, every layer: the blocks walk the list of pairs (32 of them per look) and share the pieces of every
+// copy to be made, so that a list without any costs a launch and one load.
+constexpr int kPiece = kThreads * 8;   // 16-byte vectors of a page that a block moves at a time
+template <typename Pair> __device__ __forceinline__ void copy_pages(const KvView &c, int n, Pair pair) {
+  const int lane = threadIdx.x & 31;
+  const int64_t per = 2 * c.half_elems() / 8, pieces = (per + kPiece - 1) / kPiece;   // per page
+  uint4 *pool = reinterpret_cast<uint4 *>(c.pool);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    int src = -1, dst = -1;
+    if (i0 + lane < n) pair(i0 + lane, &src, &dst);
+    const unsigned todo = __ballot_sync(0xffffffffu, src >= 0 && dst >= 0 && src != dst);
+    const int64_t each = pieces * c.layers, all = each * __popc(todo);
+    for (int64_t x = blockIdx.x; x < all; x += gridDim.x) {
+      const int nth = int(x / each), from = int(__fns(todo, 0, nth + 1));   // the nth pair to be copied
+      const int64_t s = __shfl_sync(0xffffffffu, src, from), d = __shfl_sync(0xffffffffu, dst, from);
+      const int64_t y0 = x - nth * each, layer = y0 / pieces, v0 = (y0 - layer * pieces) * kPiece + threadIdx.x;
+      uint4 *base = pool + layer * (c.layer_elems() / 8);
+      uint4 v[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        if (v0 + y * kThreads < per) v[y] = base[s * per + v0 + y * kThreads];
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        if (v0 + y * kThreads < per) base[d * per + v0 + y * kThreads] = v[y];
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) kv_cow_kernel(const KvView c, const int32_t *__restrict__ cow, int n) {
   pdl_enter();
-  for (int i = blockIdx.z; i < n; i += gridDim.z)
-    if (cow[2 * i] >= 0) copy_page(c, cow[2 * i], cow[2 * i + 1]);
+  copy_pages(c, n, [&](int i, int *s, int *d) {
+    *s = cow[2 * i];
+    *d = cow[2 * i + 1];
+  });
 }
 
 __global__ void __launch_bounds__(kThreads) kv_copy_kernel(const KvView c, const int32_t *__restrict__ src,
                                                            const int32_t *__restrict__ dst, int n) {
   pdl_enter();
-  for (int i = blockIdx.z; i < n; i += gridDim.z) {
-    const int s = valid_page(c, src[i]), d = valid_page(c, dst[i]);
-    if (s >= 0 && d >= 0 && s != d) copy_page(c, s, d);
-  }
+  copy_pages(c, n, [&](int i, int *s, int *d) {
+    *s = valid_page(c, src[i]);
+    *d = valid_page(c, dst[i]);
+  });
 }
 
 // One block per pair.
@@ -327,7 +355,7 @@ struct Rows {
 // A thread owns one unit (see rope.cu) of kItems of a token's 2 kv_heads + q_heads heads on one layer.  Where the
 // token goes (its sequence, slot and page) is worked out once per block and token, under the latency of the
 // data's loads.  grid: (units, layers).
-template <typename T, int V, int kItems>
+template <typename T, int V, int MODE, int kItems>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, const Rows r, int units, int turned) {
   pdl_enter();
   __shared__ int64_t slot_of[kThreads + 1];   // element offset in a layer of K of head 0, -1: not written
@@ -338,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, con
   const unsigned in = unsigned(x - t * per), group = in / unsigned(units);
   const int unit = int(in - group * unsigned(units)), h0 = int(group) * kItems;
   const bool have = t < r.T;
-  RopeUnit<T, V> u[kItems];
+  RopeUnit<T, V, MODE> u[kItems];
   const int layer = int(blockIdx.y);
   if (have) {
     const T *k = reinterpret_cast<const T *>(r.k) + layer * r.kl + t * r.kt;
@@ -349,12 +377,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, con
       const int h = h0 + i;
       if (h < heads)
         u[i].load(h < H ? k + int64_t(h) * D : (h < 2 * H ? v + int64_t(h - H) * D : q + int64_t(h - 2 * H) * D), unit, turned,
-                  r.rot, r.inter);
+                  r.rot);
     }
   }
-  Angles<V> g;
-  if (have && unit < turned && r.cos_sin)
-    load_angles<V>(g, r.cos_sin, r.n_pos, __ldg(r.pos + t), r.rot, r.inter, unit, 0, [] {
+  Angles<V, MODE> g;
+  if (MODE != kRopeNone && have && unit < turned)
+    load_angles<V, MODE>(g, r.cos_sin, r.n_pos, __ldg(r.pos + t), r.rot, unit, 0, [] {
       if (MOE_CHECKED) check_fail(kCheckPos);
     });
   const int64_t tk = t0 + threadIdx.x;   // the block's tokens
@@ -380,11 +408,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvView c, con
     const int h = h0 + i;
     if (h >= 2 * H) {
       if (h < heads)
-        u[i].store(reinterpret_cast<T *>(r.q_out) + (t * r.q_heads + (h - 2 * H)) * D, unit, turned, r.rot, r.inter, g);
+        u[i].store(reinterpret_cast<T *>(r.q_out) + (t * r.q_heads + (h - 2 * H)) * D, unit, turned, r.rot, g);
     } else if (slot >= 0) {
       T *dst = pool + int64_t(h) * c.page_size() * D;
-      if (h < H) u[i].store(dst, unit, turned, r.rot, r.inter, g);
-      else u[i].copy(dst, unit, turned, r.rot, r.inter);
+      if (h < H) u[i].store(dst, unit, turned, r.rot, g);
+      else u[i].copy(dst, unit, turned, r.rot);
     }
   }
 }
@@ -399,8 +427,9 @@ int check_ids(const void *a, const void *b, int64_t n) {
   return MOE_OK;
 }
 
+// Blocks of a page-copy kernel for at most n copies: enough to fill the SMs, no more than there are pieces.
 dim3 page_grid(const KvView &c, int64_t n) {
-  return dim3(clamp_grid(cdiv(2 * c.half_elems() / 8, kThreads * 4), 64), unsigned(c.layers), clamp_grid(n, 65535));
+  return dim3(clamp_grid(cdiv(2 * c.half_elems() / 8, kPiece) * c.layers * n, int64_t(num_sms()) * 8));
 }
 
 }  // namespace
@@ -543,30 +572,21 @@ extern "C" int moe_kv_append(const moe_kv_desc *desc, const moe_kv *kv, int64_t 
   a.n_pos = r.n_pos;
   // without rotation every vector is a copy
   const int V = r.cos_sin ? rope_vec(2, r.rot, r.interleaved) : 8;
-  const int units = rope_units(V, int(desc->head_dim), int(a.rot), a.inter);
-  const int turned = int((a.inter ? a.rot : a.rot / 2) / V);
+  const int units = rope_units(V, int(desc->head_dim), a.rot, a.inter);   // rot 0 without rotation
+  const int turned = (a.inter ? a.rot : a.rot / 2) / V;
   const int64_t heads = 2 * desc->kv_heads + a.q_heads;
-  // several rows a thread in large calls, as in moe_rope
-  const int items = a.inter || turned == 0 ? 8 : 4;
-  const bool many = r.T * heads * units * n_layers >= int64_t(num_sms()) * 1024 * items;
+  const int mode = !a.cos_sin ? kRopeNone : (a.inter ? kRopeInter : kRopeHalf);
+  const bool many = r.T * heads * units * n_layers >= int64_t(num_sms()) * 1024 * (mode == kRopeHalf ? 4 : 8);   // as in moe_rope
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  auto go = [&](auto zero, auto vec, auto per) -> int {
-    const int64_t blocks = cdiv(r.T * cdiv(heads, int64_t(decltype(per)::value)) * units, kThreads);
-    MOE_SUPPORT(blocks < (int64_t(1) << 31), "T * heads too large");
-    launch_pdl(kv_append_kernel<decltype(zero), decltype(vec)::value, decltype(per)::value>, dim3(unsigned(blocks), unsigned(n_layers)),
-               dim3(kThreads), 0, st, c, a, units, turned);
-    return MOE_OK;
+  auto typed = [&](auto zero) -> int {
+    return rope_dispatch<2>(mode, V, many, [&](auto m, auto vec, auto per) -> int {
+      const int64_t blocks = cdiv(r.T * cdiv(heads, int64_t(decltype(per)::value)) * units, kThreads);
+      MOE_SUPPORT(blocks < (int64_t(1) << 31), "T * heads too large");
+      launch_pdl(kv_append_kernel<decltype(zero), decltype(vec)::value, decltype(m)::value, decltype(per)::value>,
+                 dim3(unsigned(blocks), unsigned(n_layers)), dim3(kThreads), 0, st, c, a, units, turned);
+      return MOE_OK;
+    });
   };
-  auto with_heads = [&](auto zero, auto vec) {
-    if (!many) return go(zero, vec, std::integral_constant<int, 1>());
-    return items == 8 ? go(zero, vec, std::integral_constant<int, 8>()) : go(zero, vec, std::integral_constant<int, 4>());
-  };
-  auto with_vec = [&](auto zero) -> int {
-    if (V == 8) return with_heads(zero, std::integral_constant<int, 8>());
-    if (V == 4) return with_heads(zero, std::integral_constant<int, 4>());
-    if (V == 2) return with_heads(zero, std::integral_constant<int, 2>());
-    return with_heads(zero, std::integral_constant<int, 1>());
-  };
-  MOE_TRY(desc->dtype == MOE_F16 ? with_vec(__half{}) : with_vec(__nv_bfloat16{}));
+  MOE_TRY(desc->dtype == MOE_F16 ? typed(__half{}) : typed(__nv_bfloat16{}));
   return check_launch("kv_append");
 }

@@ -2,6 +2,8 @@
 // geometry on the device, the row -> sequence search and the rotation of one pair.
 #pragma once
 
+#include <type_traits>
+
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -83,6 +85,8 @@ inline int rope_vec(int elem_bytes, int64_t rot, int interleaved) {
   return v;   // interleaved: rot is even, so at least 2
 }
 
+enum : int { kRopeNone = 0, kRopeHalf = 1, kRopeInter = 2 };   // none: heads are copied
+
 // Units of a head: its rotated vectors (pairs of vectors in the half layout), then the vectors that are copied.
 __host__ __device__ inline int rope_units(int V, int head_dim, int rot, int inter) {
   return (inter ? rot : rot / 2) / V + (head_dim - rot) / V;
@@ -90,78 +94,74 @@ __host__ __device__ inline int rope_units(int V, int head_dim, int rot, int inte
 
 // The cosines and sines of one unit: V of each (half layout) or V / 2 (interleaved).  NaN for positions outside
 // the table.
-template <int V> struct Angles {
-  float c[V], s[V];
+template <int V, int MODE> struct Angles {
+  static constexpr int kN = MODE == kRopeNone ? 0 : (MODE == kRopeInter ? V / 2 : V);
+  float c[kN > 0 ? kN : 1], s[kN > 0 ? kN : 1];
 };
-template <int V, typename Bad>
-__device__ __forceinline__ void load_angles(Angles<V> &a, const float *cos_sin, int64_t n_pos, int p, int rot, int inter,
-                                            int unit, int inverse, Bad bad) {
-  const int n = inter ? V / 2 : V;
+template <int V, int MODE, typename Bad>
+__device__ __forceinline__ void load_angles(Angles<V, MODE> &a, const float *cos_sin, int64_t n_pos, int p, int rot, int unit,
+                                            int inverse, Bad bad) {
+  constexpr int n = Angles<V, MODE>::kN;
   const bool inside = p >= 0 && p < n_pos;
   if (!inside) bad();
   const float *row = cos_sin + int64_t(inside ? p : 0) * rot + unit * n;
   // rows start at multiples of rot, even: pairs are read together where rot / 2 is even too
-  if (V >= 4 && (rot & 3) == 0) {
+  if (n >= 2 && (rot & 3) == 0) {
 #pragma unroll
-    for (int i = 0; i + 1 < V; i += 2)
-      if (i < n) {
-        const float2 c = __ldg(reinterpret_cast<const float2 *>(row + i));
-        const float2 s = __ldg(reinterpret_cast<const float2 *>(row + rot / 2 + i));
-        a.c[i] = c.x;
-        a.c[i + 1] = c.y;
-        a.s[i] = s.x;
-        a.s[i + 1] = s.y;
-      }
+    for (int i = 0; i + 1 < n; i += 2) {
+      const float2 c = __ldg(reinterpret_cast<const float2 *>(row + i));
+      const float2 s = __ldg(reinterpret_cast<const float2 *>(row + rot / 2 + i));
+      a.c[i] = c.x;
+      a.c[i + 1] = c.y;
+      a.s[i] = s.x;
+      a.s[i + 1] = s.y;
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < n) {
-        a.c[i] = __ldg(row + i);
-        a.s[i] = __ldg(row + rot / 2 + i);
-      }
+    for (int i = 0; i < n; ++i) {
+      a.c[i] = __ldg(row + i);
+      a.s[i] = __ldg(row + rot / 2 + i);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (i < n) {
-      a.c[i] = inside ? a.c[i] : NAN;
-      a.s[i] = inside ? (inverse ? -a.s[i] : a.s[i]) : NAN;
-    }
+  for (int i = 0; i < n; ++i) {
+    a.c[i] = inside ? a.c[i] : NAN;
+    a.s[i] = inside ? (inverse ? -a.s[i] : a.s[i]) : NAN;
+  }
 }
 
 // One unit: (a, b) -> (a c - b s, a s + b c) in fp32, one rounding; units past the rotated ones are copied.
-template <typename T, int V> struct RopeUnit {
+template <typename T, int V, int MODE> struct RopeUnit {
   Pack<T, V> a, b;
-  __device__ __forceinline__ void load(const T *src, int unit, int turned, int rot, int inter) {
-    if (unit < turned) {
+  __device__ __forceinline__ void load(const T *src, int unit, int turned, int rot) {
+    if (MODE != kRopeNone && unit < turned) {
       a.load(src + unit * V);
-      if (!inter) b.load(src + rot / 2 + unit * V);
+      if (MODE == kRopeHalf) b.load(src + rot / 2 + unit * V);
     } else {
       a.load(src + rot + (unit - turned) * V);
     }
   }
-  __device__ __forceinline__ void copy(T *dst, int unit, int turned, int rot, int inter) const {   // the unit as it is
-    if (unit >= turned) {
+  __device__ __forceinline__ void copy(T *dst, int unit, int turned, int rot) const {   // the unit as it is
+    if (MODE == kRopeNone || unit >= turned) {
       a.store(dst + rot + (unit - turned) * V);
     } else {
       a.store(dst + unit * V);
-      if (!inter) b.store(dst + rot / 2 + unit * V);
+      if (MODE == kRopeHalf) b.store(dst + rot / 2 + unit * V);
     }
   }
-  __device__ __forceinline__ void store(T *dst, int unit, int turned, int rot, int inter, const Angles<V> &g) const {
-    if (unit >= turned) {
+  __device__ __forceinline__ void store(T *dst, int unit, int turned, int rot, const Angles<V, MODE> &g) const {
+    if (MODE == kRopeNone || unit >= turned) {
       a.store(dst + rot + (unit - turned) * V);
-    } else if (inter) {
-      if constexpr (V > 1) {
-        Pack<T, V> y;
+    } else if constexpr (MODE == kRopeInter) {
+      Pack<T, V> y;
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          const float x0 = a.get(2 * i), x1 = a.get(2 * i + 1);
-          y.set(2 * i, x0 * g.c[i] - x1 * g.s[i]);
-          y.set(2 * i + 1, x0 * g.s[i] + x1 * g.c[i]);
-        }
-        y.store(dst + unit * V);
+      for (int i = 0; i < V / 2; ++i) {
+        const float x0 = a.get(2 * i), x1 = a.get(2 * i + 1);
+        y.set(2 * i, x0 * g.c[i] - x1 * g.s[i]);
+        y.set(2 * i + 1, x0 * g.s[i] + x1 * g.c[i]);
       }
-    } else {
+      y.store(dst + unit * V);
+    } else if constexpr (MODE == kRopeHalf) {
       Pack<T, V> y, z;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -174,5 +174,25 @@ template <typename T, int V> struct RopeUnit {
     }
   }
 };
+
+// Launch helper: go(MODE, V, items a thread) as compile-time constants.  items: 128 bytes of loads (a unit of the half
+// layout is two vectors) in large calls, one unit in small ones.
+template <int BYTES, typename Go> int rope_dispatch(int mode, int V, bool many, Go go) {
+  auto with = [&](auto m, auto v) -> int {
+    constexpr int kMany = decltype(m)::value == kRopeHalf ? 4 : 8;
+    return many ? go(m, v, std::integral_constant<int, kMany>()) : go(m, v, std::integral_constant<int, 1>());
+  };
+  auto with_vec = [&](auto m) -> int {
+    if constexpr (BYTES == 2)
+      if (V == 8) return with(m, std::integral_constant<int, 8>());
+    if (V == 4) return with(m, std::integral_constant<int, 4>());
+    if constexpr (decltype(m)::value == kRopeHalf)
+      if (V == 1) return with(m, std::integral_constant<int, 1>());
+    return with(m, std::integral_constant<int, 2>());
+  };
+  if (mode == kRopeNone) return with(std::integral_constant<int, kRopeNone>(), std::integral_constant<int, 16 / BYTES>());
+  if (mode == kRopeHalf) return with_vec(std::integral_constant<int, kRopeHalf>());
+  return with_vec(std::integral_constant<int, kRopeInter>());
+}
 
 }  // namespace moe

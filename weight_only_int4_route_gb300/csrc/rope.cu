@@ -3,8 +3,6 @@
 // A pair (a, b) of a head turns by its position's angle: (a cos - b sin, a sin + b cos); turning back
 // (sin -> -sin) is the gradient.  The angles are formed and reduced in 64 bits when the table is made:
 // position times frequency reaches 10^5 radians, where a 32-bit product is off by 10^-2.
-#include <type_traits>
-
 #include "kv_internal.cuh"
 
 namespace moe {
@@ -46,11 +44,11 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(int64_t n_pos, int
 // A thread owns one unit (a 16-byte vector, or a pair of them) of kHeads heads of one token: the angles
 // are read once for them, and their loads are in flight together.  Consecutive threads own consecutive
 // vectors of a head.  Bound by memory: nothing is read twice but the table, and it stays in the caches.
-template <typename T, int V, int kHeads>
+template <typename T, int V, int MODE, int kHeads>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const T *x, int64_t xt, int64_t xh,
                                                         const int32_t *__restrict__ pos,
                                                         const float *__restrict__ cos_sin, int64_t n_pos, int64_t T_,
-                                                        int heads, int rot, int units, int turned, int inter, int inverse,
+                                                        int heads, int rot, int units, int turned, int inverse,
                                                         T *out, int64_t ot, int64_t oh) {
   pdl_enter();
   const unsigned groups = unsigned(heads + kHeads - 1) / kHeads, per = groups * unsigned(units);
@@ -62,19 +60,19 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const T *x, int64_t xt, 
   const int unit = int(in - group * unsigned(units)), h0 = int(group) * kHeads;
   const int p = __ldg(pos + t);   // first: the angles wait for it
   const T *src = x + t * xt + h0 * xh;
-  RopeUnit<T, V> u[kHeads];
+  RopeUnit<T, V, MODE> u[kHeads];
 #pragma unroll
   for (int i = 0; i < kHeads; ++i)
-    if (h0 + i < heads) u[i].load(src + i * xh, unit, turned, rot, inter);
-  Angles<V> g;
+    if (h0 + i < heads) u[i].load(src + i * xh, unit, turned, rot);
+  Angles<V, MODE> g;
   if (unit < turned)
-    load_angles<V>(g, cos_sin, n_pos, p, rot, inter, unit, inverse, [] {
+    load_angles<V, MODE>(g, cos_sin, n_pos, p, rot, unit, inverse, [] {
       if (MOE_CHECKED) check_fail(kCheckPos);
     });
   T *dst = out + t * ot + h0 * oh;
 #pragma unroll
   for (int i = 0; i < kHeads; ++i)
-    if (h0 + i < heads) u[i].store(dst + i * oh, unit, turned, rot, inter, g);
+    if (h0 + i < heads) u[i].store(dst + i * oh, unit, turned, rot, g);
 }
 
 unsigned grid_for(int64_t work) {
@@ -135,26 +133,17 @@ extern "C" int moe_rope(const void *x, int dtype, int64_t T, int64_t heads, int6
   // memory with too little in flight, and more would spend themselves on indices (one head a thread: 45 us
   // instead of 27 on 8192 x 32 heads of f16, interleaved)
   const bool many = T * heads * units >= int64_t(num_sms()) * 1024 * (interleaved ? 8 : 4);
-  auto go = [&](auto zero, auto vec, auto per) -> int {
+  auto typed = [&](auto zero) -> int {
     using E = decltype(zero);
-    const int64_t blocks = cdiv(T * cdiv(heads, int64_t(decltype(per)::value)) * units, kThreads);
-    MOE_SUPPORT(blocks < (int64_t(1) << 31), "T * heads too large");
-    launch_pdl(rope_kernel<E, decltype(vec)::value, decltype(per)::value>, dim3(unsigned(blocks)), dim3(kThreads), 0, st,
-               static_cast<const E *>(x), x_token_stride, x_head_stride, pos, cos_sin, n_pos, T, int(heads), int(rot), units,
-               turned, interleaved, inverse, static_cast<E *>(out), out_token_stride, out_head_stride);
-    return MOE_OK;
+    return rope_dispatch<int(sizeof(E))>(interleaved ? kRopeInter : kRopeHalf, V, many, [&](auto mode, auto vec, auto per) -> int {
+      const int64_t blocks = cdiv(T * cdiv(heads, int64_t(decltype(per)::value)) * units, kThreads);
+      MOE_SUPPORT(blocks < (int64_t(1) << 31), "T * heads too large");
+      launch_pdl(rope_kernel<E, decltype(vec)::value, decltype(mode)::value, decltype(per)::value>, dim3(unsigned(blocks)),
+                 dim3(kThreads), 0, st, static_cast<const E *>(x), x_token_stride, x_head_stride, pos, cos_sin, n_pos, T,
+                 int(heads), int(rot), units, turned, inverse, static_cast<E *>(out), out_token_stride, out_head_stride);
+      return MOE_OK;
+    });
   };
-  auto with_heads = [&](auto zero, auto vec) {
-    if (!many) return go(zero, vec, std::integral_constant<int, 1>());
-    return interleaved ? go(zero, vec, std::integral_constant<int, 8>()) : go(zero, vec, std::integral_constant<int, 4>());
-  };
-  auto with_vec = [&](auto zero) -> int {
-    if constexpr (sizeof(zero) == 2)
-      if (V == 8) return with_heads(zero, std::integral_constant<int, 8>());
-    if (V == 4) return with_heads(zero, std::integral_constant<int, 4>());
-    if (V == 2) return with_heads(zero, std::integral_constant<int, 2>());
-    return with_heads(zero, std::integral_constant<int, 1>());
-  };
-  MOE_TRY(dtype == MOE_F16 ? with_vec(__half{}) : (dtype == MOE_BF16 ? with_vec(__nv_bfloat16{}) : with_vec(float{})));
+  MOE_TRY(dtype == MOE_F16 ? typed(__half{}) : (dtype == MOE_BF16 ? typed(__nv_bfloat16{}) : typed(float{})));
   return check_launch("rope");
 }
