@@ -68,7 +68,7 @@ constexpr float kLazy = 8.f;
 // What an item costs beside its key tiles (its queries, its first tiles' latency, its epilogue), in key
 // tiles: shares are dealt with it counted in.  Not in calls so small that every key tile gets a CTA
 // of its own (up to kSmallUnits units per CTA): there the longest share decides.
-constexpr int kItemCost = 3, kSmallUnits = 4;
+constexpr int kItemCost = 4, kSmallUnits = 4;
 enum : int { kErrQ = 11, kErrKv = 12, kErrS = 13, kErrP = 14, kErrO = 15, kErrX = 16, kErrDrain = 17 };
 
 struct Rows {
@@ -321,6 +321,11 @@ struct Walk {
     open(r);
     if (cnt == 0) left = 0;   // only a share's last units can be overhead alone: the item is the next CTA's
   }
+  // The first key tile that some row of stream st does not see whole.
+  __device__ __forceinline__ int edge(const Rows &r, bool wide, int st) const {
+    if (s.keys == 0) return 0;
+    return (r.mask ? s.start : min(s.start + tile * tokens + (wide ? st * r.tile_tokens : 0) + 1, s.keys)) / kTile;
+  }
   // Key tiles of stream st in this piece.  wide: the row tile's own limit; narrow: alternate tiles.
   __device__ __forceinline__ int stream_tiles(const Rows &r, bool wide, int st) const {
     if (!wide) return (cnt + 1 - st) >> 1;
@@ -459,6 +464,24 @@ __device__ __forceinline__ void tc_ld_row(uint32_t taddr, float (&v)[kTile]) {
         "=f"(v[107]), "=f"(v[108]), "=f"(v[109]), "=f"(v[110]), "=f"(v[111]), "=f"(v[112]), "=f"(v[113]),
         "=f"(v[114]), "=f"(v[115]), "=f"(v[116]), "=f"(v[117]), "=f"(v[118]), "=f"(v[119]), "=f"(v[120]),
         "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]), "=f"(v[126]), "=f"(v[127])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_ld_half(uint32_t taddr, float (&v)[kTile / 2]) {   // 64 columns
+  asm volatile(
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64 + 32];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]),
+        "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
+        "=f"(v[30]), "=f"(v[31]), "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]),
+        "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]),
+        "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]), "=f"(v[49]), "=f"(v[50]),
+        "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]), "=f"(v[57]),
+        "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
       : "r"(taddr)
       : "memory");
 }
@@ -719,10 +742,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         live = any != 0;
       }
       const bool work = __any_sync(0xffffffffu, live);
-      // causal: keys this row sees; the tiles from `edge` on are not seen whole by every row of the stream
+      // keys this row may see
       const int lim = keys == 0 ? 0 : (r.mask ? keys : min(start + tok + 1, keys));
-      const int edge = keys == 0 ? 0
-                       : (r.mask ? start : min(start + tok - tok_in + 1, keys)) / kTile;
+      const int edge = w.edge(r, WIDE, st);
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i) {
         const int j = WIDE ? i : 2 * i + st, tile = t0 + j;
@@ -751,6 +773,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 see &= word;
               }
               if (!live) see = 0;
+              if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
 #pragma unroll
               for (int y = 0; y < 32; ++y) v[32 * x + y] = (see >> y) & 1u ? v[32 * x + y] : -INFINITY;
             }
@@ -795,29 +818,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tc_wait_st();
         }
         if (tile >= edge) {
-          // V rows that some row must not see: what lies past the keys is zeroed, and so is
-          // what is not finite among the new tokens (0 x NaN would reach every row); rows that do
-          // see those get them added in the epilogue
+          // V rows that some row must not see: what lies past the keys is zeroed, and so is what is not finite among the new
+          // tokens (0 x NaN would reach every row); rows that do see those get them added in the epilogue
+          constexpr uint32_t kExp = (kF16 ? 0x7C00u : 0x7F80u) * 0x10001u, kLow = (kF16 ? 0x0400u : 0x0080u) * 0x10001u;
           const uint32_t vi = tiles + j;
           if (!(ok = wait(&kv_full[kS + vi % kS], vi / kS, kErrKv))) break;
-          uint8_t *vt = base + S::kRing + (kS + vi % kS) * kTB + row * 128;
-          const int key = tile * kTile + row;
+          const int key = tile * kTile + row;   // this thread's row of the V tile
           if (key >= start) {
-            const bool past = key >= keys;
-            for (int x = 0; x < DP / 8; ++x) {
-              uint4 *q = reinterpret_cast<uint4 *>(vt + (x >> 3) * kTile * 128) + ((x ^ row) & 7);
-              constexpr uint32_t kExp = kF16 ? 0x7C00u : 0x7F80u;
-              uint32_t e[4] = {q->x, q->y, q->z, q->w};
-              bool bad = past;
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                if ((e[y] & kExp) == kExp) bad = true, e[y] &= 0xffff0000u;
-                if ((e[y] & (kExp << 16)) == (kExp << 16)) bad = true, e[y] &= 0x0000ffffu;
+            for (int h = 0; h < DP / 64; ++h) {
+              uint4 *q = reinterpret_cast<uint4 *>(base + S::kRing + (kS + vi % kS) * kTB + (h * kTile + row) * 128);
+              uint4 e[8];
+              uint32_t bad = 0;   // an exponent of all ones plus its lowest bit carries into the sign's place
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                e[x] = q[(x ^ row) & 7];
+                bad |= ((e[x].x & kExp) + kLow) | ((e[x].y & kExp) + kLow) | ((e[x].z & kExp) + kLow) | ((e[x].w & kExp) + kLow);
               }
-              if (bad) {
-                if (!past) *poison = 1;
-                *q = past ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(e[0], e[1], e[2], e[3]);
-              }
+              if (key < keys && (bad & 0x80008000u) == 0) continue;
+              if (key < keys) *poison = 1;
+              auto clean = [&](uint32_t v) {   // 0 past the keys, and in place of what is not finite
+                const uint32_t high = ((v & kExp) + kLow) & 0x80008000u;
+                return key < keys ? v & ~(high | (high - (high >> 15))) : 0u;
+              };
+#pragma unroll
+              for (int x = 0; x < 8; ++x) q[(x ^ row) & 7] = make_uint4(clean(e[x].x), clean(e[x].y), clean(e[x].z), clean(e[x].w));
             }
           }
           asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -877,30 +902,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
       for (int y = 0; y < 4; ++y)
         to[y] = r.out + __shfl_sync(0xffffffffu, prow_h, 8 * y + (lane >> 2)) * D + 8 * (lane & 3);
-      for (int x0 = WIDE ? 0 : kCols * st; x0 < ksteps * 16; x0 += WIDE ? kCols : 2 * kCols) {
-        float o[kCols];
-        __syncwarp();
-        if (WIDE) {
-          if (n > 0 && work) tc_ld32(t_o + x0, o);
-          if (n == 0 || l == 0.f) {
-#pragma unroll
-            for (int y = 0; y < kCols; ++y) o[y] = 0.f;
-          }
-        } else {
-          if (work) tc_ld32(tmem + lanes + 2 * kTile + x0, o);
-#pragma unroll
-          for (int y = 0; y < kCols; ++y) o[y] = f[0] == 0.f ? 0.f : o[y] * f[0];
-          if (n1 > 0 && work) {
-            float o1[kCols];
-            tc_ld32(tmem + lanes + 2 * kTile + DP + x0, o1);
-#pragma unroll
-            for (int y = 0; y < kCols; ++y) o[y] = f[1] == 0.f ? o[y] : fmaf(o1[y], f[1], o[y]);
-          }
-        }
+      // columns x0 .. x0 + 31 of the output row
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      auto emit = [&](int x0, const float *o) {
         if (whole) {
           // through shared memory, so that a store instruction covers 64 bytes of 8 rows: 16 bytes of 32
           // rows each would take the L1 32 lines an instruction
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+          __syncwarp();
           uint8_t *sw = stage + lane * (kCols * 2);
 #pragma unroll
           for (int y = 0; y < kCols / 8; ++y)
@@ -919,6 +927,35 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           float *dst = ws.o + part * DP + int64_t(x0) * kPartRows + part_row;
 #pragma unroll
           for (int y = 0; y < kCols; ++y) dst[y * kPartRows] = o[y];
+        }
+      };
+      if constexpr (WIDE) {
+        float o[DP];
+        const bool some = n > 0 && work;
+        if (some) {
+          if constexpr (DP == kTile) tc_ld_row(t_o, o);
+          else tc_ld_half(t_o, o);
+        }
+        if (!some || l == 0.f) {
+#pragma unroll
+          for (int y = 0; y < DP; ++y) o[y] = 0.f;
+        }
+#pragma unroll
+        for (int x0 = 0; x0 < DP; x0 += kCols)
+          if (x0 < ksteps * 16) emit(x0, o + x0);
+      } else {
+        for (int x0 = kCols * st; x0 < ksteps * 16; x0 += 2 * kCols) {
+          float o[kCols], o1[kCols];
+          __syncwarp();
+          if (work) tc_ld32(tmem + lanes + 2 * kTile + x0, o);
+#pragma unroll
+          for (int y = 0; y < kCols; ++y) o[y] = f[0] == 0.f ? 0.f : o[y] * f[0];
+          if (n1 > 0 && work) {
+            tc_ld32(tmem + lanes + 2 * kTile + DP + x0, o1);
+#pragma unroll
+            for (int y = 0; y < kCols; ++y) o[y] = f[1] == 0.f ? o[y] : fmaf(o1[y], f[1], o[y]);
+          }
+          emit(x0, o);
         }
       }
       if (*poison) {
