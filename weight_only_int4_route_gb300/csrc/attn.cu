@@ -170,12 +170,15 @@ __device__ __forceinline__ int64_t key_tiles_before(const Rows &r, const Seq &s,
   return n;
 }
 
-// Exclusive prefix sums of two values over the block; returns the totals.
+// Exclusive prefix sums of two values over the first kPlaceThreads threads of the block (whole warps, which alone
+// call it); returns the totals.
+constexpr int kPlaceThreads = 256;
+__device__ __forceinline__ void place_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(kPlaceThreads) : "memory"); }
 struct Pair64 {
   int64_t a, b;
 };
 __device__ __forceinline__ Pair64 block_scan_pair(Pair64 v, Pair64 *before, Pair64 *scratch /*[32]*/) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = kPlaceThreads / 32;
   Pair64 x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -186,13 +189,13 @@ __device__ __forceinline__ Pair64 block_scan_pair(Pair64 v, Pair64 *before, Pair
     }
   }
   if (lane == 31) scratch[warp] = x;
-  __syncthreads();
+  place_sync();
   Pair64 base = {0, 0}, total = {0, 0};
   for (int w = 0; w < nw; ++w) {
     if (w < warp) base = {base.a + scratch[w].a, base.b + scratch[w].b};
     total = {total.a + scratch[w].a, total.b + scratch[w].b};
   }
-  __syncthreads();
+  place_sync();
   *before = {base.a + x.a - v.a, base.b + x.b - v.b};
   return total;
 }
@@ -210,9 +213,9 @@ struct Place {
   }
 };
 
-// Every thread of the block calls it; sh is shared.
+// The first kPlaceThreads threads call it; sh is shared, and complete after the next barrier of the block.
 __device__ void find_place(const KvView &c, const Rows &r, int tokens, Place *sh, Pair64 *scratch) {
-  const int tid = threadIdx.x, nt = blockDim.x, H = c.kv_heads;
+  const int tid = threadIdx.x, nt = kPlaceThreads, H = c.kv_heads;
   auto count = [&](int b) -> Pair64 {   // key tiles and items of sequence b
     if (b >= r.n) return {0, 0};
     const Seq s = load_seq(c, r, tokens, b);
@@ -266,7 +269,6 @@ __device__ void find_place(const KvView &c, const Rows &r, int tokens, Place *sh
       base += sum.a + cost * sum.b;
     }
   }
-  __syncthreads();
 }
 
 // Walks the pieces of items in the CTA's share; every warp walks the same way.  The walk lives in shared
@@ -531,11 +533,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tokens = WIDE ? 2 * r.tile_tokens : r.tile_tokens;   // tokens of an item
-  if (warp == 0) {   // under the latency of the index loads below
+  // warps 0-7 find the CTA's work while the others set up what every CTA needs
+  if (warp < kPlaceThreads / 32) {
+    find_place(c, r, tokens, place, scratch);
+  } else if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(tmem_slot)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
-  }
-  if (tid == 32) {
+  } else if (warp == kLoadWarp && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_free[i], 1);
@@ -556,15 +560,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     ws.piece[2 * blockIdx.x].valid = 0;
     ws.piece[2 * blockIdx.x + 1].valid = 0;
   }
-  find_place(c, r, tokens, place, scratch);
-  Walk &w = walks[warp];   // find_place ends with a barrier
-  if (lane == 0) w.begin(c, r, tokens, *place);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  Walk &w = walks[warp];
+  if (lane == 0) w.begin(c, r, tokens, *place);
+  __syncwarp();
   const uint32_t tmem = *tmem_slot;
   if (place->units == 0) {
-    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+    if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
     return;
   }
   const int ksteps = (c.head_dim + 15) / 16;   // 16-wide steps of head_dim that hold anything
@@ -1009,7 +1013,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
 }
 
 // Join the pieces of the item that CTA blockIdx.x began and did not finish, in the order of the CTAs
