@@ -59,6 +59,8 @@ def rope(x: torch.Tensor, pos: torch.Tensor, cos_sin: torch.Tensor, interleaved:
     _ints(pos)
     xt, xh, x1 = x.stride()
     ot, oh, o1 = out.stride()
+    if T == 1:
+        xt = ot = H * D                                # torch leaves the stride of a dimension of one open
     assert x1 == 1 and o1 == 1 and out.shape == x.shape and out.dtype == x.dtype
     assert pos.numel() == T and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()
     n_pos, rot = cos_sin.shape
@@ -185,7 +187,7 @@ def attention(q: torch.Tensor, cache: KVCache, cu: torch.Tensor, seqs: torch.Ten
     _ints(cu, seqs, start)
     n = seqs.numel()
     assert start.numel() == n and cu.numel() == n + 1
-    assert D == cache.head_dim and q.dtype == cache.pool.dtype and qh == D and q1 == 1
+    assert D == cache.head_dim and q.dtype == cache.pool.dtype and (qh == D or H == 1) and q1 == 1
     words, bits = 0, None
     if mask is not None:
         _ints(mask)

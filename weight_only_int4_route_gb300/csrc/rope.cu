@@ -137,7 +137,7 @@ extern "C" int moe_rope(const void *x, int dtype, int64_t T, int64_t heads, int6
     using E = decltype(zero);
     return rope_dispatch<int(sizeof(E))>(interleaved ? kRopeInter : kRopeHalf, V, many, [&](auto mode, auto vec, auto per) -> int {
       const int64_t blocks = cdiv(T * cdiv(heads, int64_t(decltype(per)::value)) * units, kThreads);
-      MOE_SUPPORT(blocks < (int64_t(1) << 31), "T * heads too large");
+      MOE_SUPPORT(blocks < (int64_t(1) << 31) && heads * units < (int64_t(1) << 31), "T * heads too large");
       launch_pdl(rope_kernel<E, decltype(vec)::value, decltype(mode)::value, decltype(per)::value>, dim3(unsigned(blocks)),
                  dim3(kThreads), 0, st, static_cast<const E *>(x), x_token_stride, x_head_stride, pos, cos_sin, n_pos, T,
                  int(heads), int(rot), units, turned, inverse, static_cast<E *>(out), out_token_stride, out_head_stride);
