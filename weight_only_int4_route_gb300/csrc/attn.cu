@@ -378,15 +378,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return y;
 }
 
-// D (tensor memory) (+)= A (tensor memory) x B (shared memory)
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
 // One lane of the warp, the same one each time; the compiler knows that a single thread runs what follows and
 // keeps descriptors in uniform registers, where the MMA instructions take them from.
 __device__ __forceinline__ bool elect_one() {
@@ -395,19 +386,78 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// The 16-wide steps of head_dim of one scores tile: both operands K-major in 64-element swizzle columns.
+// The 16-wide steps of head_dim of one scores tile: both operands K-major in 64-element swizzle columns (step i
+// starts 32 bytes further, from the fifth on in the next 16 KB).  A whole tile's MMAs are one statement: the single
+// issuing thread's instructions are what two streams' tiles wait for.  Only the descriptors' low words change: their
+// address field cannot carry (shared addresses stay below 256 KB).
 template <int STEPS>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc, int steps) {
-#pragma unroll
-  for (int i = 0; i < STEPS; ++i) {
+  static_assert(STEPS == 4 || STEPS == 8, "head_dim up to 64 or 128");
+  if (steps == STEPS) {
+    if constexpr (STEPS == 8)
+      asm volatile(
+        "{\n .reg .pred t, f;\n .reg .b32 ql, kl;\n .reg .b64 qd, kd;\n setp.ne.b32 f, 0, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " add.u32 ql, %1, 0;\n add.u32 kl, %3, 0;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, f;\n"
+        " add.u32 ql, %1, 2;\n add.u32 kl, %3, 2;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, t;\n"
+        " add.u32 ql, %1, 4;\n add.u32 kl, %3, 4;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, t;\n"
+        " add.u32 ql, %1, 6;\n add.u32 kl, %3, 6;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, t;\n"
+        " add.u32 ql, %1, 1024;\n add.u32 kl, %3, 1024;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, t;\n"
+        " add.u32 ql, %1, 1026;\n add.u32 kl, %3, 1026;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, t;\n"
+        " add.u32 ql, %1, 1028;\n add.u32 kl, %3, 1028;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, t;\n"
+        " add.u32 ql, %1, 1030;\n add.u32 kl, %3, 1030;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, t;\n"
+        "}\n" ::"r"(d), "r"(uint32_t(q)), "r"(uint32_t(q >> 32)), "r"(uint32_t(k)), "r"(uint32_t(k >> 32)), "r"(idesc)
+        : "memory");
+    else
+      asm volatile(
+        "{\n .reg .pred t, f;\n .reg .b32 ql, kl;\n .reg .b64 qd, kd;\n setp.ne.b32 f, 0, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " add.u32 ql, %1, 0;\n add.u32 kl, %3, 0;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, f;\n"
+        " add.u32 ql, %1, 2;\n add.u32 kl, %3, 2;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, t;\n"
+        " add.u32 ql, %1, 4;\n add.u32 kl, %3, 4;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, t;\n"
+        " add.u32 ql, %1, 6;\n add.u32 kl, %3, 6;\n mov.b64 qd, {ql, %2};\n mov.b64 kd, {kl, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], qd, kd, %5, t;\n"
+        "}\n" ::"r"(d), "r"(uint32_t(q)), "r"(uint32_t(q >> 32)), "r"(uint32_t(k)), "r"(uint32_t(k >> 32)), "r"(idesc)
+        : "memory");
+    return;
+  }
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
     const uint64_t off = uint64_t(((i >> 2) * kTile * 128 + (i & 3) * 32) >> 4);
-    if (i < steps) tc_mma_ss(d, q + off, k + off, idesc, i != 0);
+    tc_mma_ss(d, q + off, k + off, idesc, i != 0);
   }
 }
 // The eight 16-key steps of one output tile: weights in tensor memory, V N-major.
-__device__ __forceinline__ void mma_output(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, bool acc) {
-#pragma unroll
-  for (int i = 0; i < kTile / 16; ++i) tc_mma_ts(d, p + 8 * i, v + uint64_t((i * 16 * 128) >> 4), idesc, i != 0 || acc);
+__device__ __forceinline__ void mma_output(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred t, p;\n .reg .b32 a, vl;\n .reg .b64 vd;\n setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " add.u32 a, %1, 0;\n add.u32 vl, %2, 0;\n mov.b64 vd, {vl, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a], vd, %4, p;\n"
+      " add.u32 a, %1, 8;\n add.u32 vl, %2, 128;\n mov.b64 vd, {vl, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a], vd, %4, t;\n"
+      " add.u32 a, %1, 16;\n add.u32 vl, %2, 256;\n mov.b64 vd, {vl, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a], vd, %4, t;\n"
+      " add.u32 a, %1, 24;\n add.u32 vl, %2, 384;\n mov.b64 vd, {vl, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a], vd, %4, t;\n"
+      " add.u32 a, %1, 32;\n add.u32 vl, %2, 512;\n mov.b64 vd, {vl, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a], vd, %4, t;\n"
+      " add.u32 a, %1, 40;\n add.u32 vl, %2, 640;\n mov.b64 vd, {vl, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a], vd, %4, t;\n"
+      " add.u32 a, %1, 48;\n add.u32 vl, %2, 768;\n mov.b64 vd, {vl, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a], vd, %4, t;\n"
+      " add.u32 a, %1, 56;\n add.u32 vl, %2, 896;\n mov.b64 vd, {vl, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a], vd, %4, t;\n"
+      "}\n" ::"r"(d), "r"(p), "r"(uint32_t(v)), "r"(uint32_t(v >> 32)), "r"(idesc), "r"(acc)
+      : "memory");
 }
 
 // V tile as the B operand of the second product: N = head_dim is the contiguous direction (128-byte
@@ -673,34 +723,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int n0 = w.stream_tiles(r, WIDE, 0), n1 = w.stream_tiles(r, WIDE, 1);
         const int events = WIDE ? 2 * w.cnt : w.cnt;
         ok = wait(&q_full[qb], WIDE ? items : items >> 1, kErrQ);
-        auto scores = [&](int e) -> bool {
-          const int st = e & 1;
-          const uint32_t ks = kc % kS;
+        const uint64_t q0 = q_desc + uint64_t(qb * (kTB >> 4)), q1 = q0 + uint64_t(WIDE ? kTB >> 4 : 0);
+        uint32_t ks = kc % kS, vs = vc % kS, kp = kc / kS, vp = vc / kS;   // stages and their uses
+        auto step = [](uint32_t &stage, uint32_t &use) {
+          if (++stage == kS) {
+            stage = 0;
+            ++use;
+          }
+        };
+        // i: the stream's tile; st is a constant in every copy of these (an index into registers)
+        auto scores = [&](int st, int i) -> bool {
           if (!WIDE || st == 0) {
-            if (!wait(&kv_full[ks], kc / kS, kErrKv)) return false;
+            if (!wait(&kv_full[ks], kp, kErrKv)) return false;
             tc_fence_after();
           }
-          if ((e >> 1) < (st ? n1 : n0)) {
-            mma_scores<DP / 16>(tmem + st * kTile, q_desc + uint64_t((WIDE ? st : qb) * (kTB >> 4)),
-                                k_desc + uint64_t(ks * (kTB >> 4)), id_s, ksteps);
+          if (i < (st ? n1 : n0)) {
+            mma_scores<DP / 16>(tmem + st * kTile, st ? q1 : q0, k_desc + uint64_t(ks * (kTB >> 4)), id_s, ksteps);
             tc_commit(&s_full[st]);
           }
           if (!WIDE || st == 1) {
             tc_commit(&kv_free[ks]);
-            ++kc;
+            step(ks, kp);
           }
-          if (e + 1 == events) tc_commit(&q_free[qb]);   // the item's last scores: Q may be replaced
           return true;
         };
-        for (int e = 0; ok && e < 2 && e < events; ++e) ok = scores(e);
-        for (int e = 0; ok && e < events; ++e) {
-          const int st = e & 1, i = e >> 1, n = st ? n1 : n0;
-          const uint32_t vs = vc % kS;
+        auto output = [&](int st, int i) -> bool {
           if (!WIDE || st == 0)
-            if (!(ok = wait(&kv_full[kS + vs], vc / kS, kErrKv))) break;
+            if (!wait(&kv_full[kS + vs], vp, kErrKv)) return false;
+          const int n = st ? n1 : n0;
           if (i < n) {
-            if (i == 0 && !(ok = wait(&o_free[st], no[st] + 1, kErrO))) break;
-            if (!(ok = wait(&p_ready[st], np[st], kErrP))) break;
+            if (i == 0 && !wait(&o_free[st], no[st] + 1, kErrO)) return false;
+            if (!wait(&p_ready[st], np[st], kErrP)) return false;
             ++np[st];
             tc_fence_after();
             mma_output(tmem + 2 * kTile + st * DP, tmem + st * kTile, v0_desc + uint64_t(vs * (kTB >> 4)), id_o, i != 0);
@@ -711,10 +764,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           if (!WIDE || st == 1) {
             tc_commit(&kv_free[kS + vs]);
-            ++vc;
+            step(vs, vp);
           }
-          if (e + 2 < events) ok = scores(e + 2);
+          return true;
+        };
+        for (int i = -1; ok && 2 * i < events; ++i) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const int e = 2 * i + st;
+            if (i >= 0 && e < events) ok = ok && output(st, i);
+            if (e + 2 < events) {
+              ok = ok && scores(st, i + 1);
+              if (e + 3 == events) tc_commit(&q_free[qb]);   // the item's last scores: Q may be replaced
+            }
+          }
         }
+        kc += w.cnt;
+        vc += w.cnt;
       }
       tc_commit(drain);
       volatile int never = 0;
