@@ -616,9 +616,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   Walk &w = walks[warp];
   if (lane == 0) w.begin(c, r, tokens, *place);
   __syncwarp();
-  const uint32_t tmem = *tmem_slot;
+  // read anew by every role: a register kept across them would be spilled, and with shared memory taking nearly all
+  // of the L1 a spilled value comes from the L2
+  const volatile uint32_t *tmem_base = tmem_slot;
   if (place->units == 0) {
-    if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+    if (warp == kMmaWarp)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(*tmem_base), "r"(512u));
     return;
   }
   const int ksteps = (c.head_dim + 15) / 16;   // 16-wide steps of head_dim that hold anything
@@ -635,7 +638,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ------------------------------------------------ copies: a lane per page of a tile
     const int ps = c.page_size(), per = ps < kTile ? kTile / ps : 1, box = min(ps, kTile);
     const int halves = DP / 64;
-    uint32_t count[2] = {0, 0};
+    uint32_t k_count = 0, v_count = 0;
     bool ok = true;
     for (; ok && w.more(); next_item()) {
       const int cnt = w.cnt, t0 = w.t0, keys = w.s.keys, head = w.head;
@@ -649,11 +652,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (MOE_CHECKED) check_fail(kCheckPage);
         return c.pages;
       };
-      auto copy = [&](int j, int page, int v) -> bool {
-        const uint32_t i = count[v], s = v * kS + i % kS;
+      auto copy = [&](int j, int page, int v, uint32_t &count) -> bool {
+        const uint32_t i = count, s = v * kS + i % kS;
         if (!wait(&kv_free[s], i / kS + 1, kErrKv)) return false;
         if (lane == 0) mbar_expect_tx(&kv_full[s], kTB);
-        count[v] = i + 1;
+        count = i + 1;
         __syncwarp();
         if (lane < per) {
           const uint32_t dst = su32(base + S::kRing + s * kTB) + lane * box * 128;
@@ -666,20 +669,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       };
       // in the order of their use: K0 K1 V0 K2 V1 ...
       int p0 = page_of(0), p1 = page_of(1);
-      ok = copy(0, p0, 0);
+      ok = copy(0, p0, 0, k_count);
       for (int j = 0; ok && j < cnt; ++j) {
-        if (j + 1 < cnt) ok = copy(j + 1, p1, 0);
+        if (j + 1 < cnt) ok = copy(j + 1, p1, 0, k_count);
         const int p2 = page_of(j + 2);
-        ok = ok && copy(j, p0, 1);
+        ok = ok && copy(j, p0, 1, v_count);
         p0 = p1;
         p1 = p2;
       }
     }
     if (lane == 0) {   // every copy must have landed before the CTA exits, also where another role gave up
       volatile int never = 0;
-      for (int v = 0; v < 2; ++v)
-        for (uint32_t i = count[v] > kS ? count[v] - kS : 0; i < count[v]; ++i)
-          mbar_wait(&kv_full[v * kS + i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
+      for (uint32_t i = k_count > kS ? k_count - kS : 0; i < k_count; ++i)
+        mbar_wait(&kv_full[i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
+      for (uint32_t i = v_count > kS ? v_count - kS : 0; i < v_count; ++i)
+        mbar_wait(&kv_full[kS + i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
     }
     __syncwarp();
   } else if (warp == kQWarp) {
@@ -712,11 +716,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // the first two events, then per event its second product and the scores of the event after next
     // (the same stream's next tile, which may overwrite the weights just used: MMAs run in order).
     if (elect_one()) {
+      const uint32_t tmem = *tmem_base;
       const int bf = kF16 ? 0 : 1;
       const uint32_t id_s = idesc_f16(bf, kTile, kTile), id_o = idesc_f16(bf, kTile, ksteps * 16) | kTransposeB;
       const uint64_t q_desc = sw128_desc(su32(base + S::kQ)), k_desc = sw128_desc(su32(base + S::kRing)),
                      v0_desc = v_desc(su32(base + S::kRing + kS * kTB));
-      uint32_t kc = 0, vc = 0, items = 0, np[2] = {0, 0}, no[2] = {0, 0};
+      // barriers by their shared-memory addresses
+      const uint32_t bars = su32(bar), b_kv_full = bars + 4 * 8, b_kv_free = b_kv_full + 2 * kS * 8, b_s_full = b_kv_free + 2 * kS * 8,
+                     b_p_ready = b_s_full + 16, b_o_full = b_p_ready + 16, b_o_free = b_o_full + 16;
+      auto wait_at = [&](uint32_t b, uint32_t parity, int code) {
+        return mbar_wait_at(b, parity & 1, abort_flag, code, &g_attn_error);
+      };
+      uint32_t items = 0, ks = 0, vs = 0, kp = 0, vp = 0;   // the rings' next stages and the parities of their uses
+      uint32_t phases = 0;   // bit st: p_ready, bit 2 + st: o_free (an array would live in local memory)
+      auto step = [](uint32_t &stage, uint32_t &use) {
+        stage = stage + 1 == kS ? 0 : stage + 1;
+        use ^= stage == 0 ? 1 : 0;
+      };
       bool ok = true;
       for (; ok && w.more(); w.next(c, r), ++items) {
         const int qb = WIDE ? 0 : items & 1;
@@ -724,46 +740,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int events = WIDE ? 2 * w.cnt : w.cnt;
         ok = wait(&q_full[qb], WIDE ? items : items >> 1, kErrQ);
         const uint64_t q0 = q_desc + uint64_t(qb * (kTB >> 4)), q1 = q0 + uint64_t(WIDE ? kTB >> 4 : 0);
-        uint32_t ks = kc % kS, vs = vc % kS, kp = kc / kS, vp = vc / kS;   // stages and their uses
-        auto step = [](uint32_t &stage, uint32_t &use) {
-          if (++stage == kS) {
-            stage = 0;
-            ++use;
-          }
-        };
         // i: the stream's tile; st is a constant in every copy of these (an index into registers)
         auto scores = [&](int st, int i) -> bool {
           if (!WIDE || st == 0) {
-            if (!wait(&kv_full[ks], kp, kErrKv)) return false;
+            if (!wait_at(b_kv_full + ks * 8, kp, kErrKv)) return false;
             tc_fence_after();
           }
           if (i < (st ? n1 : n0)) {
             mma_scores<DP / 16>(tmem + st * kTile, st ? q1 : q0, k_desc + uint64_t(ks * (kTB >> 4)), id_s, ksteps);
-            tc_commit(&s_full[st]);
+            tc_commit_at(b_s_full + st * 8);
           }
           if (!WIDE || st == 1) {
-            tc_commit(&kv_free[ks]);
+            tc_commit_at(b_kv_free + ks * 8);
             step(ks, kp);
           }
           return true;
         };
         auto output = [&](int st, int i) -> bool {
           if (!WIDE || st == 0)
-            if (!wait(&kv_full[kS + vs], vp, kErrKv)) return false;
+            if (!wait_at(b_kv_full + (kS + vs) * 8, vp, kErrKv)) return false;
           const int n = st ? n1 : n0;
           if (i < n) {
-            if (i == 0 && !wait(&o_free[st], no[st] + 1, kErrO)) return false;
-            if (!wait(&p_ready[st], np[st], kErrP)) return false;
-            ++np[st];
+            if (i == 0 && !wait_at(b_o_free + st * 8, (phases >> (2 + st)) ^ 1, kErrO)) return false;
+            if (!wait_at(b_p_ready + st * 8, phases >> st, kErrP)) return false;
+            phases ^= 1u << st;
             tc_fence_after();
             mma_output(tmem + 2 * kTile + st * DP, tmem + st * kTile, v0_desc + uint64_t(vs * (kTB >> 4)), id_o, i != 0);
             if (i + 1 == n) {
-              tc_commit(&o_full[st]);
-              ++no[st];
+              tc_commit_at(b_o_full + st * 8);
+              phases ^= 4u << st;
             }
           }
           if (!WIDE || st == 1) {
-            tc_commit(&kv_free[kS + vs]);
+            tc_commit_at(b_kv_free + (kS + vs) * 8);
             step(vs, vp);
           }
           return true;
@@ -779,8 +788,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
         }
-        kc += w.cnt;
-        vc += w.cnt;
       }
       tc_commit(drain);
       volatile int never = 0;
@@ -791,6 +798,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
     // ------------------------------------------------ softmax and epilogue
+    const uint32_t tmem = *tmem_base;
     const int st = warp >> 2, q4 = warp & 3, row = q4 * 32 + lane;
     const int tok_in = row / r.group, g = row - tok_in * r.group;
     const uint32_t lanes = uint32_t(q4 * 32) << 16;
@@ -929,7 +937,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       // the running maximum that goes with l and O as they are
       float ref = m == -INFINITY ? -INFINITY : m - kShift;
-      float f[2] = {1.f, 0.f};   // narrow: factors of the two streams' outputs
+      float f0 = 1.f, f1 = 0.f;   // narrow: factors of the two streams' outputs
       const int n1 = WIDE ? 0 : w.cnt >> 1;
       if constexpr (WIDE) {
         if (n > 0) {
@@ -947,9 +955,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ++nx;
         const float2 b = mine[(st ^ 1) * kTile];
         const float top = fmaxf(ref, b.x);
-        f[st] = ref == -INFINITY ? 0.f : ex2(ref - top);
-        f[st ^ 1] = b.x == -INFINITY ? 0.f : ex2(b.x - top);
-        l = st == 0 ? l * f[0] + b.y * f[1] : b.y * f[0] + l * f[1];
+        const float fm = ref == -INFINITY ? 0.f : ex2(ref - top), fo = b.x == -INFINITY ? 0.f : ex2(b.x - top);
+        f0 = st == 0 ? fm : fo;
+        f1 = st == 0 ? fo : fm;
+        l = st == 0 ? l * f0 + b.y * f1 : b.y * f0 + l * f1;   // the same sum in both warps
         ref = top;
         if (!(ok = wait(&o_full[0], no[0], kErrO))) break;
         ++no[0];
@@ -1019,11 +1028,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           __syncwarp();
           if (work) tc_ld32(tmem + lanes + 2 * kTile + x0, o);
 #pragma unroll
-          for (int y = 0; y < kCols; ++y) o[y] = f[0] == 0.f ? 0.f : o[y] * f[0];
+          for (int y = 0; y < kCols; ++y) o[y] = f0 == 0.f ? 0.f : o[y] * f0;
           if (n1 > 0 && work) {
             tc_ld32(tmem + lanes + 2 * kTile + DP + x0, o1);
 #pragma unroll
-            for (int y = 0; y < kCols; ++y) o[y] = f[1] == 0.f ? o[y] : fmaf(o1[y], f[1], o[y]);
+            for (int y = 0; y < kCols; ++y) o[y] = f1 == 0.f ? o[y] : fmaf(o1[y], f1, o[y]);
           }
           emit(x0, o);
         }
@@ -1079,7 +1088,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(*tmem_base), "r"(512u));
 }
 
 // Join the pieces of the item that CTA blockIdx.x began and did not finish, in the order of the CTAs

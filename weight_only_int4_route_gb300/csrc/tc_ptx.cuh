@@ -61,6 +61,31 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity, volatile
   }
 }
 
+// The same on a shared-memory address (no generic address arithmetic on a single thread's critical path).
+__device__ __forceinline__ bool mbar_try_at(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(addr), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_at(uint32_t addr, uint32_t parity, volatile int *abort_flag, int code, int *error) {
+  if (mbar_try_at(addr, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_at(addr, parity)) return true;
+    if ((it & 7) == 0) {
+      if (*abort_flag) return false;
+      if (clock64() - t0 > kTimeoutCycles) {
+        *abort_flag = 1;
+        atomicExch(error, code);
+        return false;
+      }
+    }
+  }
+}
+
 // ---- CTA pairs (clusters of two): addresses in the peer CTA, remote arrivals, cluster barrier
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -103,6 +128,9 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(su32(bar))
                : "memory");
+}
+__device__ __forceinline__ void tc_commit_at(uint32_t addr) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(addr) : "memory");
 }
 // pairs: completion of the pair's MMAs issued so far, signalled on `bar` in both CTAs / in this one
 __device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
