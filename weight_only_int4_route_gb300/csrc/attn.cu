@@ -58,7 +58,7 @@ constexpr int kAttnThreads = 32 * 12;      // the third warpgroup: copies, MMA i
 // Registers: 384 threads launch with 168 each; the softmax warpgroups (a row of 128 scores per thread)
 // take over what the third does not need: 2 x 224 + 56 = 3 x 168.
 constexpr int kSoftRegs = 224, kOtherRegs = 56;
-constexpr int kRingBytes = 128 << 10;      // K and V tiles in flight, half of it each
+constexpr int kRingBytes = 128 << 10;      // K and V tiles in flight
 constexpr int kCols = 32;                  // columns of the output that the epilogue handles at a time
 constexpr int kStageBytes = 32 * kCols * 2;   // a softmax warp's 16-bit output rows of those columns
 // The running maximum is only moved when a tile exceeds it by more than this (in powers of two):
@@ -542,9 +542,9 @@ __device__ __forceinline__ void tc_ld_half(uint32_t taddr, float (&v)[kTile / 2]
 // streams' maxima and sums for the narrow merge, the softmax warps' output staging, barriers.
 template <int DP> struct Smem {
   static constexpr int kTileBytes = kTile * DP * 2;
-  static constexpr int kStages = kRingBytes / kTileBytes / 2;   // of the K ring, and of the V ring
+  static constexpr int kStages = kRingBytes / kTileBytes / 2;   // each a K tile and a V tile
   static constexpr int kQ = 0, kRing = 2 * kTileBytes, kXml = kRing + kRingBytes, kStage = kXml + 4 * kTile * 8,
-                       kScratch = kStage + kSoftWarps * kStageBytes, kBar = kScratch + 32 * 16, kBars = 2 + 2 + 4 * kStages + 4 * 2 + 4 + 1;
+                       kScratch = kStage + kSoftWarps * kStageBytes, kBar = kScratch + 32 * 16, kBars = 2 + 2 + 2 * kStages + 4 * 2 + 4 + 1;
   static constexpr int kPlace = kBar + kBars * 8, kWalks = kPlace + int(sizeof(Place)),
                        kFlags = kWalks + kAttnThreads / 32 * int(sizeof(Walk));
   static constexpr int kBytes = kFlags + 16 + 1024 /* alignment */;
@@ -563,6 +563,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   pdl_enter();
   using S = Smem<DP>;
   constexpr int kS = S::kStages, kTB = S::kTileBytes;
+  // Copy p of a piece brings K of key tile p and V of key tile p - kLag: what the MMA thread uses together (the second
+  // product of one tile, and the scores of the stream's next one), so it waits and lets go once for both.
+  constexpr int kLag = WIDE ? 1 : 2;
   constexpr bool kF16 = std::is_same<T, __half>::value;
   // weights are exp2(s - max + kShift): f16 keeps small weights away from its underflow (the largest,
   // 2^(8 + 7), stays below 65504); bf16 has fp32's range
@@ -571,7 +574,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
   float2 *xml = reinterpret_cast<float2 *>(base + S::kXml);
   uint64_t *bar = reinterpret_cast<uint64_t *>(base + S::kBar);
-  uint64_t *q_full = bar, *q_free = bar + 2, *kv_full = bar + 4, *kv_free = kv_full + 2 * kS, *s_full = kv_free + 2 * kS,
+  uint64_t *q_full = bar, *q_free = bar + 2, *kv_full = bar + 4, *kv_free = kv_full + kS, *s_full = kv_free + kS,
            *p_ready = s_full + 2, *o_full = p_ready + 2, *o_free = o_full + 2, *x_full = o_free + 2,
            *drain = x_full + 4;
   Pair64 *scratch = reinterpret_cast<Pair64 *>(base + S::kScratch);
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&o_full[i], 1);
       mbar_init(&o_free[i], WIDE ? 4 : 8);
     }
-    for (int i = 0; i < 2 * kS; ++i) {   // K stages, then V stages
+    for (int i = 0; i < kS; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_free[i], 1);
     }
@@ -638,7 +641,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ------------------------------------------------ copies: a lane per page of a tile
     const int ps = c.page_size(), per = ps < kTile ? kTile / ps : 1, box = min(ps, kTile);
     const int halves = DP / 64;
-    uint32_t k_count = 0, v_count = 0;
+    uint32_t count = 0;
     bool ok = true;
     for (; ok && w.more(); next_item()) {
       const int cnt = w.cnt, t0 = w.t0, keys = w.s.keys, head = w.head;
@@ -652,38 +655,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (MOE_CHECKED) check_fail(kCheckPage);
         return c.pages;
       };
-      auto copy = [&](int j, int page, int v, uint32_t &count) -> bool {
-        const uint32_t i = count, s = v * kS + i % kS;
-        if (!wait(&kv_free[s], i / kS + 1, kErrKv)) return false;
-        if (lane == 0) mbar_expect_tx(&kv_full[s], kTB);
-        count = i + 1;
+      int page = page_of(0), page1 = c.pages, page2 = c.pages;   // of key tiles p, p - 1, p - 2
+      for (int p = 0; p < cnt + kLag; ++p, ++count) {
+        const uint32_t s = count % kS;
+        const int next = page_of(p + 1);
+        if (!(ok = wait(&kv_free[s], count / kS + 1, kErrKv))) break;
+        const bool k = p < cnt, v = p >= kLag;
+        if (lane == 0) mbar_expect_tx(&kv_full[s], (k ? kTB : 0) + (v ? kTB : 0));
         __syncwarp();
         if (lane < per) {
-          const uint32_t dst = su32(base + S::kRing + s * kTB) + lane * box * 128;
-          const int slot = ((t0 + j) * kTile) & (ps - 1);   // nonzero in 256-token pages only
+          const uint32_t dst = su32(base + S::kRing + s * 2 * kTB) + lane * box * 128;
+          auto copy = [&](int j, uint32_t to, int pg, int which) {
+            const int slot = ((t0 + j) * kTile) & (ps - 1);   // nonzero in 256-token pages only
 #pragma unroll
-          for (int h = 0; h < halves; ++h)
-            tma_load_4d(dst + h * kTile * 128, &map_kv, 64 * h, slot, head, 2 * page + v, &kv_full[s]);
+            for (int h = 0; h < halves; ++h)
+              tma_load_4d(to + h * kTile * 128, &map_kv, 64 * h, slot, head, 2 * pg + which, &kv_full[s]);
+          };
+          if (k) copy(p, dst, page, 0);
+          if (v) copy(p - kLag, dst + kTB, WIDE ? page1 : page2, 1);
         }
-        return true;
-      };
-      // in the order of their use: K0 K1 V0 K2 V1 ...
-      int p0 = page_of(0), p1 = page_of(1);
-      ok = copy(0, p0, 0, k_count);
-      for (int j = 0; ok && j < cnt; ++j) {
-        if (j + 1 < cnt) ok = copy(j + 1, p1, 0, k_count);
-        const int p2 = page_of(j + 2);
-        ok = ok && copy(j, p0, 1, v_count);
-        p0 = p1;
-        p1 = p2;
+        page2 = page1;
+        page1 = page;
+        page = next;
       }
     }
     if (lane == 0) {   // every copy must have landed before the CTA exits, also where another role gave up
       volatile int never = 0;
-      for (uint32_t i = k_count > kS ? k_count - kS : 0; i < k_count; ++i)
+      for (uint32_t i = count > kS ? count - kS : 0; i < count; ++i)
         mbar_wait(&kv_full[i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
-      for (uint32_t i = v_count > kS ? v_count - kS : 0; i < v_count; ++i)
-        mbar_wait(&kv_full[kS + i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
     }
     __syncwarp();
   } else if (warp == kQWarp) {
@@ -720,19 +719,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int bf = kF16 ? 0 : 1;
       const uint32_t id_s = idesc_f16(bf, kTile, kTile), id_o = idesc_f16(bf, kTile, ksteps * 16) | kTransposeB;
       const uint64_t q_desc = sw128_desc(su32(base + S::kQ)), k_desc = sw128_desc(su32(base + S::kRing)),
-                     v0_desc = v_desc(su32(base + S::kRing + kS * kTB));
+                     v0_desc = v_desc(su32(base + S::kRing + kTB));
       // barriers by their shared-memory addresses
-      const uint32_t bars = su32(bar), b_kv_full = bars + 4 * 8, b_kv_free = b_kv_full + 2 * kS * 8, b_s_full = b_kv_free + 2 * kS * 8,
+      const uint32_t bars = su32(bar), b_kv_full = bars + 4 * 8, b_kv_free = b_kv_full + kS * 8, b_s_full = b_kv_free + kS * 8,
                      b_p_ready = b_s_full + 16, b_o_full = b_p_ready + 16, b_o_free = b_o_full + 16;
       auto wait_at = [&](uint32_t b, uint32_t parity, int code) {
         return mbar_wait_at(b, parity & 1, abort_flag, code, &g_attn_error);
       };
-      uint32_t items = 0, ks = 0, vs = 0, kp = 0, vp = 0;   // the rings' next stages and the parities of their uses
+      uint32_t items = 0, stage = 0, use = 0;   // the ring's present stage and its use's parity
       uint32_t phases = 0;   // bit st: p_ready, bit 2 + st: o_free (an array would live in local memory)
-      auto step = [](uint32_t &stage, uint32_t &use) {
-        stage = stage + 1 == kS ? 0 : stage + 1;
-        use ^= stage == 0 ? 1 : 0;
-      };
       bool ok = true;
       for (; ok && w.more(); w.next(c, r), ++items) {
         const int qb = WIDE ? 0 : items & 1;
@@ -741,39 +736,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ok = wait(&q_full[qb], WIDE ? items : items >> 1, kErrQ);
         const uint64_t q0 = q_desc + uint64_t(qb * (kTB >> 4)), q1 = q0 + uint64_t(WIDE ? kTB >> 4 : 0);
         // i: the stream's tile; st is a constant in every copy of these (an index into registers)
-        auto scores = [&](int st, int i) -> bool {
-          if (!WIDE || st == 0) {
-            if (!wait_at(b_kv_full + ks * 8, kp, kErrKv)) return false;
-            tc_fence_after();
-          }
+        auto scores = [&](int st, int i) {
           if (i < (st ? n1 : n0)) {
-            mma_scores<DP / 16>(tmem + st * kTile, st ? q1 : q0, k_desc + uint64_t(ks * (kTB >> 4)), id_s, ksteps);
+            mma_scores<DP / 16>(tmem + st * kTile, st ? q1 : q0, k_desc + uint64_t(stage * (2 * kTB >> 4)), id_s, ksteps);
             tc_commit_at(b_s_full + st * 8);
           }
-          if (!WIDE || st == 1) {
-            tc_commit_at(b_kv_free + ks * 8);
-            step(ks, kp);
-          }
-          return true;
         };
         auto output = [&](int st, int i) -> bool {
-          if (!WIDE || st == 0)
-            if (!wait_at(b_kv_full + (kS + vs) * 8, vp, kErrKv)) return false;
           const int n = st ? n1 : n0;
           if (i < n) {
             if (i == 0 && !wait_at(b_o_free + st * 8, (phases >> (2 + st)) ^ 1, kErrO)) return false;
             if (!wait_at(b_p_ready + st * 8, phases >> st, kErrP)) return false;
             phases ^= 1u << st;
             tc_fence_after();
-            mma_output(tmem + 2 * kTile + st * DP, tmem + st * kTile, v0_desc + uint64_t(vs * (kTB >> 4)), id_o, i != 0);
+            mma_output(tmem + 2 * kTile + st * DP, tmem + st * kTile, v0_desc + uint64_t(stage * (2 * kTB >> 4)), id_o, i != 0);
             if (i + 1 == n) {
               tc_commit_at(b_o_full + st * 8);
               phases ^= 4u << st;
             }
-          }
-          if (!WIDE || st == 1) {
-            tc_commit_at(b_kv_free + (kS + vs) * 8);
-            step(vs, vp);
           }
           return true;
         };
@@ -781,10 +761,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             const int e = 2 * i + st;
-            if (i >= 0 && e < events) ok = ok && output(st, i);
+            if (!ok || e >= events) break;
+            if (!WIDE || st == 0) {
+              if (!(ok = wait_at(b_kv_full + stage * 8, use, kErrKv))) break;
+              tc_fence_after();
+            }
+            if (i >= 0 && !(ok = output(st, i))) break;
             if (e + 2 < events) {
-              ok = ok && scores(st, i + 1);
+              scores(st, i + 1);
               if (e + 3 == events) tc_commit(&q_free[qb]);   // the item's last scores: Q may be replaced
+            }
+            if (!WIDE || st == 1) {
+              tc_commit_at(b_kv_free + stage * 8);
+              stage = stage + 1 == kS ? 0 : stage + 1;
+              use ^= stage == 0 ? 1 : 0;
             }
           }
         }
@@ -805,7 +795,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t t_s = tmem + lanes + st * kTile, t_o = tmem + lanes + 2 * kTile + st * DP;
     const int D = c.head_dim;
     uint8_t *stage = base + S::kStage + warp * kStageBytes;
-    uint32_t tiles = 0, ns = 0, no[2] = {0, 0}, nx = 0;   // tiles: key tiles of the pieces before
+    uint32_t copies = 0, ns = 0, no[2] = {0, 0}, nx = 0;   // copies: those of the pieces before
     bool ok = true;
     for (; ok && w.more(); next_item()) {
       const int n = w.stream_tiles(r, WIDE, st), t0 = w.t0, start = w.s.start, keys = w.s.keys;
@@ -899,13 +889,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // V rows that some row must not see: what lies past the keys is zeroed, and so is what is not finite among the new
           // tokens (0 x NaN would reach every row); rows that do see those get them added in the epilogue
           constexpr uint32_t kExp = (kF16 ? 0x7C00u : 0x7F80u) * 0x10001u, kLow = (kF16 ? 0x0400u : 0x0080u) * 0x10001u;
-          const uint32_t vi = tiles + j;
-          if (!(ok = wait(&kv_full[kS + vi % kS], vi / kS, kErrKv))) break;
+          const uint32_t vi = copies + j + kLag;
+          if (!(ok = wait(&kv_full[vi % kS], vi / kS, kErrKv))) break;
           const int key = tile * kTile + row;   // this thread's row of the V tile
           if (key >= start) {
 #pragma unroll
             for (int h = 0; h < DP / 64; ++h) {
-              uint4 *q = reinterpret_cast<uint4 *>(base + S::kRing + (kS + vi % kS) * kTB + (h * kTile + row) * 128);
+              uint4 *q = reinterpret_cast<uint4 *>(base + S::kRing + vi % kS * 2 * kTB + kTB + (h * kTile + row) * 128);
               uint4 e[8];
               uint32_t bad = 0;   // an exponent of all ones plus its lowest bit carries into the sign's place
 #pragma unroll
@@ -930,7 +920,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) mbar_arrive(&p_ready[st]);
       }
       if (!ok) break;
-      tiles += w.cnt;
+      copies += w.cnt + kLag;
       if (!live) {
         m = -INFINITY;
         l = 0.f;
