@@ -126,6 +126,9 @@ CAUSAL = [
     (H16, 16, 2, 128, 32, [9, 1], [5000, 3]),
     (B16, 8, 8, 128, 64, [1500], [0]),       # several items and several key tiles per block
     (H16, 8, 8, 64, 16, [1100, 700, 0, 300], [130, 0, 7, 1000]),
+    (B16, 6, 2, 64, 32, [1100, 300, 85], [70, 0, 3]),        # groups that do not divide a tile of rows
+    (H16, 10, 2, 96, 8, [500, 26, 600], [5, 400, 127]),
+    (B16, 14, 2, 128, 64, [37, 400], [1000, 333]),
 ]
 
 
@@ -217,6 +220,65 @@ def test_causal_rows_before_a_bad_token(attn):
     assert (out[90:, :, 5] == math.inf).all() and torch.isnan(out[90:, :, 70]).all()
 
 
+@pytest.mark.parametrize("dtype,Hq,Hk,D,new,ctx", [(B16, 4, 2, 128, [700, 90], [60, 300]), (H16, 2, 2, 64, [900], [0]),
+                                                   (B16, 8, 1, 64, [25, 3], [4000, 2000])])
+def test_bad_tokens_reach_only_later_rows(attn, dtype, Hq, Hk, D, new, ctx):
+    """V elements that are not finite, in several tiles, pieces and both row tiles of an item: a causal row is touched where it
+    sees one, and nowhere else."""
+    c = Case(attn, dtype, Hq, Hk, D, 16, new, ctx, seed=21)
+    clean, lse0 = c.run()
+    r = random.Random(4)
+    hit = {}
+    for b in range(len(new)):
+        for at in sorted(r.sample(range(new[b]), 2)):
+            d, h, bad = r.randrange(D), r.randrange(Hk), r.choice([math.nan, math.inf, -math.inf])
+            pos = ctx[b] + at
+            p = int(c.cache.table[c.slots[b], pos // 16])
+            c.cache.pool[0, p, 1, h, pos % 16, d] = bad
+            hit.setdefault((b, h, d), []).append((at, bad))
+    out, lse = c.run()
+    assert torch.equal(lse, lse0)
+    want = clean.clone()
+    grp = Hq // Hk
+    for (b, h, d), bads in hit.items():
+        for at, bad in bads:
+            want[c.cu[b] + at:c.cu[b + 1], h * grp:(h + 1) * grp, d] += bad
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out.nan_to_num(nan=0.0, posinf=1e4, neginf=-1e4), want.nan_to_num(nan=0.0, posinf=1e4, neginf=-1e4))
+
+
+def test_bad_context_reaches_every_row_but_padding(attn):
+    c = Case(attn, B16, 2, 1, 64, 16, [4], [300], seed=22)
+    c.with_sets([{0}, set(), {0, 2}, {3}], 1)
+    clean, _ = c.run()
+    p = int(c.cache.table[c.slots[0], 9])
+    c.cache.pool[0, p, 1, 0, 3, 7] = math.nan
+    out, lse = c.run()
+    assert torch.isnan(out[[0, 2, 3], :, 7]).all() and not out[1].any() and (lse[1] == -math.inf).all()
+    keep = [d for d in range(64) if d != 7]
+    assert torch.equal(out[..., keep], clean[..., keep])
+
+
+def test_extreme_values(attn):
+    """f16 values near the type's largest, all weights alike: the sum of weights is kept in range."""
+    c = Case(attn, H16, 2, 1, 64, 16, [3], [1000], seed=23, spread=0.0)
+    for i in range(c.cache.table.shape[1]):
+        p = int(c.cache.table[c.slots[0], i])
+        n = min(16, 1003 - 16 * i)
+        c.v[0][:, 16 * i:16 * i + n] = 60000.0
+        c.cache.pool[0, p, 1, :, :n] = 60000.0
+    c.check(*c.run())
+
+
+def test_one_token_of_any_stride(attn):
+    """torch leaves the stride of a dimension of one open."""
+    c = Case(attn, B16, 4, 2, 64, 16, [1], [50], seed=24)
+    out, _ = c.run()
+    odd = torch.empty(4 * 64 + 8, dtype=B16, device=DEV)[:256].as_strided((1, 4, 64), (3, 64, 1))
+    odd.copy_(c.q.to(DEV))
+    assert torch.equal(c.run(q=odd)[0], out)
+
+
 def test_large_scores(attn):
     """Scores far apart: a running maximum that grows from tile to tile, weights that underflow."""
     c = Case(attn, B16, 4, 1, 64, 16, [6], [700], seed=8, spread=1.0)
@@ -283,6 +345,14 @@ def test_many_sequences(attn):
     n = 700
     r = random.Random(3)
     c = Case(attn, B16, 2, 1, 16, 8, [r.choice([0, 1, 1, 1, 2, 5]) for _ in range(n)], [r.randint(0, 40) for _ in range(n)], seed=12)
+    c.check(*c.run())
+
+
+def test_many_prompts(attn):
+    """More prompts than a block has threads, each of several rows tiles."""
+    n = 300
+    r = random.Random(5)
+    c = Case(attn, H16, 4, 1, 16, 16, [r.choice([40, 70, 33, 1]) for _ in range(n)], [r.randint(0, 60) for _ in range(n)], seed=15)
     c.check(*c.run())
 
 

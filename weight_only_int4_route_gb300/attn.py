@@ -146,6 +146,7 @@ class KVCache:
             assert len(shape) == 3
             L, kl, vl = 1, 0, 0
         T = shape[-3]
+        kt, vt = (ks[-3], vs[-3]) if T != 1 else (H * D, H * D)
         assert start.numel() == n and cu.numel() == n + 1 and v.shape == shape and shape[-2:] == (H, D)
         assert k.dtype == v.dtype == self.pool.dtype and ks[-2:] == vs[-2:] == (D, 1)
         out, rope_args, q_args = None, (None, None, 0, 0, 0), (None, 0, 0, None)
@@ -157,8 +158,8 @@ class KVCache:
             qs, qh = q.stride(), q.shape[1]
             assert q.shape == (T, qh, D) and qs[1:] == (D, 1) and q.dtype == k.dtype
             out = torch.empty((T, qh, D), dtype=q.dtype, device=q.device)
-            q_args = (q.data_ptr(), qs[0], qh, out.data_ptr())
-        r = KvRows(k.data_ptr(), v.data_ptr(), ks[-3], kl, vs[-3], vl, cu.data_ptr(), seqs.data_ptr(), start.data_ptr(), n, T,
+            q_args = (q.data_ptr(), qs[0] if T != 1 else qh * D, qh, out.data_ptr())
+        r = KvRows(k.data_ptr(), v.data_ptr(), kt, kl, vt, vl, cu.data_ptr(), seqs.data_ptr(), start.data_ptr(), n, T,
                    *rope_args, *q_args)
         _check(lib().moe_kv_append(self._d, self._p, layer, L, ctypes.byref(r), _stream(k)), "moe_kv_append")
         return out
@@ -193,6 +194,8 @@ def attention(q: torch.Tensor, cache: KVCache, cu: torch.Tensor, seqs: torch.Ten
         _ints(mask)
         assert mask.dim() == 2 and mask.shape[0] == T
         words, bits = mask.shape[1], mask.data_ptr()
+    if T == 1:
+        qt = H * D                                     # torch leaves the stride of a dimension of one open
     L = lib()
     dev = q.device
     out = torch.empty((T, H, D), dtype=q.dtype, device=dev)

@@ -757,6 +757,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           return true;
         };
+#pragma unroll 1   // the loop shares the instruction cache with the softmax: twice its size measured 9% slower
         for (int i = -1; ok && 2 * i < events; ++i) {
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
