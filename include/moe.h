@@ -438,10 +438,11 @@ int moe_rope(const void *x, int dtype, int64_t T, int64_t heads, int64_t head_di
 /* ------------------------------------------------------------------------------------
  * Paged key/value cache.  pool: (layers, pages, 2, kv_heads, page_size, head_dim) dtype F16 | BF16,
  * K at index 0 and V at index 1 of the third dimension (a head's slots of one page are contiguous).
- * One table serves every layer: table int32 (slots, max_pages) holds the page of each page_size piece of
- * a sequence, -1 past its last; lens int32 (slots) tokens held; refs int32 (pages) how many
+ * One table serves every layer: table int32 (slots, max_pages) holds the page of each page_size
+ * piece of a sequence, -1 past its last; lens int32 (slots) tokens held; refs int32 (pages) how many
  * sequences hold a page, 0 = free.  page_size a power of two in [8, 256], head_dim % 8 == 0 and
- * <= 256, max_pages < 2^20, slots * max_pages < 2^31, pages < 2^30.  An empty cache: table all -1, lens and refs all 0.
+ * <= 256, max_pages < 2^20, slots * max_pages < 2^31, pages < 2^30.  An empty cache: table all -1,
+ * lens and refs all 0.
  * Everything is decided on the device (no host synchronization, capturable) and is independent of
  * the launch configuration: pages are taken lowest first.
  *
@@ -471,8 +472,8 @@ int moe_rope(const void *x, int dtype, int64_t T, int64_t heads, int64_t head_di
  *   cu[i] <= r < cu[i+1], goes to position start[i] + r - cu[i].  k, v: (n_layers, T, kv_heads,
  *   head_dim), token and layer strides given (multiples of 8), heads contiguous.  With cos_sin
  *   != NULL K is rotated on its way (moe_rope's arithmetic and arguments), and with q != NULL
- *   (then n_layers must be 1) q (T, q_heads, head_dim) is rotated into q_out (contiguous; may not be q).
- *   Rows of skipped sequences and positions past the table write no K or V.
+ *   (then n_layers must be 1) q (T, q_heads, head_dim) is rotated into q_out (contiguous, apart from
+ *   q).  Rows of skipped sequences and positions past the table write no K or V.
  * ------------------------------------------------------------------------------------ */
 typedef struct {
   int64_t layers, pages, page_size, kv_heads, head_dim;
@@ -515,15 +516,19 @@ int moe_kv_append(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, int6
  * kv_heads).  For a row and head, over its visible keys j:
  *   s_j = scale * q . k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = ln sum_j exp(s_j).
  * mask NULL (prompts, causal): new token t sees positions 0 .. start[i] + t.
- * mask uint32 (T, mask_words) (a tree of drafted tokens): bit j of row r (word j / 32, bit j % 32) makes
- *   new token j of the same sequence visible, and all positions before start[i] are; tokens from
+ * mask uint32 (T, mask_words) (a tree of drafted tokens): bit j of row r (word j / 32, bit j % 32)
+ *   makes new token j of the same sequence visible, and all positions before start[i] are; tokens from
  *   32 * mask_words on are visible to no row.  A row without any bit is padding and sees nothing.
- * A row that sees nothing gets out = 0 and lse = -inf.  What the cache holds where a row does not look has no
+ * Positions from max_pages * page_size on are in no cache and visible to no row; the rows of a
+ * sequence whose slot does not exist or whose start is negative or past that see nothing.  A row that
+ * sees nothing gets out = 0 and lse = -inf.  What the cache holds where a row does not look has no
  * influence on it, NaN and infinities included.  Sums and softmax statistics are fp32; the weights
  * are rounded to dtype for their product with V.
- * q: (T, q_heads, head_dim) of the cache's dtype, token stride given (a multiple of 8), heads contiguous; out:
- * contiguous; lse: fp32 (T, q_heads) or NULL.  head_dim <= 128 here, q_heads % kv_heads == 0,
- * q_heads / kv_heads <= 128.  Rows of no sequence are left as they were.
+ * q: (T, q_heads, head_dim) of the cache's dtype, token stride given (a multiple of 8, at least
+ * q_heads * head_dim), heads contiguous; out: contiguous; lse: fp32 (T, q_heads) or NULL.  head_dim
+ * <= 128 here, q_heads % kv_heads == 0, q_heads / kv_heads <= 128.  Rows of no sequence are left as
+ * they were.  Two launches; the result does not depend on the workspace's contents and is the same
+ * on every run.
  * moe_tree_mask: parents int32 (T), parents[r] = index within its sequence of row r's parent
  *   (smaller than its own), -1 = the context; anything else makes row r and its descendants padding.
  *   mask row: the token and its ancestors; pos[r] (may be NULL) = start[i] + depth (start[i] for

@@ -16,14 +16,28 @@
 //           per sequence: memory bound).
 //
 // Work: an item is (sequence, row tile or pair of them, K/V head), its units are a few units of
-// overhead (kItemCost) and its key tiles.  The units of all items, in order, are dealt to the CTAs in equal contiguous shares, whatever the lengths
-// (which only the device knows); an item cut by a share's boundary leaves partial results (running
-// maximum, sum, unscaled output) in the workspace, and a second kernel joins them in order.
+// overhead (kItemCost) and its key tiles.  The units of all items, in order, are dealt to the CTAs in
+// equal contiguous shares, whatever the lengths (which only the device knows); an item cut by a
+// share's boundary leaves partial results (running maximum, sum, unscaled output) in the workspace,
+// and a second kernel joins them in order.
 //
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = row = tensor memory lane), 8 copies of K and V
-// (a lane per page), 9 MMA issue (one thread), 10 copies of Q (one thread; apart from 8, so that the next
-// item's keys are under way while Q's buffer is still in use), 11 idle.  Tensor memory: scores S0 S1 (128 columns each, the weights replace
-// the scores' first 64), outputs O0 O1 (head_dim columns each).
+// (a lane per page), 9 MMA issue (one thread), 10 copies of Q (one thread; apart from 8, so that the
+// next item's keys are under way while Q's buffer is still in use), 11 idle.  Tensor memory: scores
+// S0 S1 (128 columns each, the weights replace the scores' first 64), outputs O0 O1 (head_dim columns
+// each): all 512 columns at head_dim 128, so a stream's next scores wait for its second product.
+//
+// Measured on GB300 (bf16, 32 query and 8 K/V heads of 128 unless said):
+//   prompt of 8191 tokens             375 us, 1465 TFLOP/s of visible pairs (0.76 of the measured matrix peak)
+//   6 prompts of 1 to 2500 tokens     216 us, 1105 TFLOP/s
+//   32 trees of 8-32 tokens over 500-8000 cached ones   106 us, 5.2 TB/s
+//   5 trees over 30000-150000 cached tokens, f16, 16 and 8 heads of 64   157 us, 5.9 TB/s
+//   one token over 1000, 16 heads     12 us for both kernels, all of it latency
+// What bounds the wide form: the chain scores -> softmax -> weights -> product of a stream takes about 2500
+// cycles, the MMAs of both streams 2050 of them; without any softmax the same loop takes 367 us.  The
+// MMA thread's waits and the instruction cache (its loop beside the softmax's) make up the rest.  The narrow
+// form reads each K and V once (DRAM bytes = the cache's), at 6.3 TB/s between a start of 4 us (finding the
+// work, first pages) and the slowest CTA's end, up to 8% after the mean.
 //
 // Every wait is bounded (see mbar_wait); when one expires the CTA records a code, drains its own copies
 // and MMAs, frees its tensor memory and returns.
@@ -493,10 +507,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 // A row of 128 scores, in one statement so that nothing uses a register before the wait.
 __device__ __forceinline__ void tc_ld_row(uint32_t taddr, float (&v)[kTile]) {
   asm volatile(
-      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%128];\n"
-      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%128 + 32];\n"
-      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%128 + 64];\n"
-      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128 + 96];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+      "[%128];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, "
+      "%43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, "
+      "%63}, [%128 + 32];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, "
+      "%75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, "
+      "%95}, [%128 + 64];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, "
+      "%106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, "
+      "%122, %123, %124, %125, %126, %127}, [%128 + 96];\n"
       " tcgen05.wait::ld.sync.aligned;\n"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
         "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
@@ -526,7 +548,8 @@ template <int DP> struct Smem {
   static constexpr int kTileBytes = kTile * DP * 2;
   static constexpr int kStages = kRingBytes / kTileBytes / 2;   // each a K tile and a V tile
   static constexpr int kQ = 0, kRing = 2 * kTileBytes, kXml = kRing + kRingBytes, kStage = kXml + 4 * kTile * 8,
-                       kScratch = kStage + kSoftWarps * kStageBytes, kBar = kScratch + 32 * 16, kBars = 2 + 2 + 2 * kStages + 4 * 2 + 4 + 1;
+                       kScratch = kStage + kSoftWarps * kStageBytes, kBar = kScratch + 32 * 16,
+                       kBars = 2 + 2 + 2 * kStages + 4 * 2 + 4 + 1;
   static constexpr int kPlace = kBar + kBars * 8, kWalks = kPlace + int(sizeof(Place)),
                        kFlags = kWalks + kAttnThreads / 32 * int(sizeof(Walk));
   static constexpr int kBytes = kFlags + 16 + 1024 /* alignment */;

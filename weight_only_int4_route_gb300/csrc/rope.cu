@@ -3,6 +3,9 @@
 // A pair (a, b) of a head turns by its position's angle: (a cos - b sin, a sin + b cos); turning back
 // (sin -> -sin) is the gradient.  The angles are formed and reduced in 64 bits when the table is made:
 // position times frequency reaches 10^5 radians, where a 32-bit product is off by 10^-2.
+//
+// Measured on GB300: 40001 tokens x 16 heads of 128 in fp32 97 us, 7.0 TB/s (the measured copy rate);
+// 8192 x 32 heads of 128 in f16, half of the head, interleaved, from a strided input 24 us, 5.7 TB/s.
 #include "kv_internal.cuh"
 
 namespace moe {
@@ -131,7 +134,7 @@ extern "C" int moe_rope(const void *x, int dtype, int64_t T, int64_t heads, int6
   // several heads a thread (128 bytes of loads: a unit of the half layout is two vectors, of the interleaved one a
   // single one) once that leaves every SM half a load of threads; fewer threads than that would wait for
   // memory with too little in flight, and more would spend themselves on indices (one head a thread: 45 us
-  // instead of 27 on 8192 x 32 heads of f16, interleaved)
+  // instead of 28 on 8192 x 32 heads of f16, interleaved)
   const bool many = T * heads * units >= int64_t(num_sms()) * 1024 * (interleaved ? 8 : 4);
   auto typed = [&](auto zero) -> int {
     using E = decltype(zero);
