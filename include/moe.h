@@ -521,9 +521,9 @@ int moe_kv_append(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, int6
  *   32 * mask_words on are visible to no row.  A row without any bit is padding and sees nothing.
  * Positions from max_pages * page_size on are in no cache and visible to no row; the rows of a
  * sequence whose slot does not exist or whose start is negative or past that see nothing.  A row that
- * sees nothing gets out = 0 and lse = -inf.  What the cache holds where a row does not look has no
- * influence on it, NaN and infinities included.  Sums and softmax statistics are fp32; the weights
- * are rounded to dtype for their product with V.
+ * sees nothing (or whose scores are all -inf) gets out = 0 and lse = -inf.  What the cache holds where
+ * a row does not look has no influence on it, NaN and infinities included.  Sums and softmax
+ * statistics are fp32; the weights are rounded to dtype for their product with V.
  * q: (T, q_heads, head_dim) of the cache's dtype, token stride given (a multiple of 8, at least
  * q_heads * head_dim), heads contiguous; out: contiguous; lse: fp32 (T, q_heads) or NULL.  head_dim
  * <= 128 here, q_heads % kv_heads == 0, q_heads / kv_heads <= 128.  Rows of no sequence are left as

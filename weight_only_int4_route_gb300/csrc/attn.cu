@@ -638,159 +638,166 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (lane == 0) w.next(c, r);
     __syncwarp();
   };
-  auto wait = [&](uint64_t *b, uint32_t parity, int code) { return mbar_wait(b, parity & 1, abort_flag, code, &g_attn_error); };
+  // a single thread's wait, and a whole warp's: there a wait that one lane gave up on has failed for all, or the lanes
+  // would part between the warp's barriers and the block's
+  auto wait = [&](uint64_t *b, uint32_t parity, int code) {
+    return mbar_wait(b, parity & 1, abort_flag, code, &g_attn_error);
+  };
+  auto wait_warp = [&](uint64_t *b, uint32_t parity, int code) {
+    return __all_sync(0xffffffffu, wait(b, parity, code)) != 0;
+  };
 
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-  if (warp == kLoadWarp) {
-    // ------------------------------------------------ copies: a lane per page of a tile
-    const int ps = c.page_size(), per = ps < kTile ? kTile / ps : 1, box = min(ps, kTile);
-    const int halves = DP / 64;
-    uint32_t count = 0;
-    bool ok = true;
-    for (; ok && w.more(); next_item()) {
-      const int cnt = w.cnt, t0 = w.t0, keys = w.s.keys, head = w.head;
-      const int32_t *tab = c.table + int64_t(w.s.slot) * c.max_pages;
-      // page of this lane's part of key tile j; c.pages (outside the map: reads as zero) past the keys
-      auto page_of = [&](int j) -> int {
-        const int key = (t0 + j) * kTile + lane * ps;
-        if (j >= cnt || lane >= per || key >= keys) return c.pages;
-        const int p = __ldg(tab + (key >> c.page_shift));
-        if (p >= 0 && p < c.pages) return p;
-        if (MOE_CHECKED) check_fail(kCheckPage);
-        return c.pages;
-      };
-      int page = page_of(0), page1 = c.pages, page2 = c.pages;   // of key tiles p, p - 1, p - 2
-      for (int p = 0; p < cnt + kLag; ++p, ++count) {
-        const uint32_t s = count % kS;
-        const int next = page_of(p + 1);
-        if (!(ok = wait(&kv_free[s], count / kS + 1, kErrKv))) break;
-        const bool k = p < cnt, v = p >= kLag;
-        if (lane == 0) mbar_expect_tx(&kv_full[s], (k ? kTB : 0) + (v ? kTB : 0));
-        __syncwarp();
-        if (lane < per) {
-          const uint32_t dst = su32(base + S::kRing + s * 2 * kTB) + lane * box * 128;
-          auto copy = [&](int j, uint32_t to, int pg, int which) {
-            const int slot = ((t0 + j) * kTile) & (ps - 1);   // nonzero in 256-token pages only
-#pragma unroll
-            for (int h = 0; h < halves; ++h)
-              tma_load_4d(to + h * kTile * 128, &map_kv, 64 * h, slot, head, 2 * pg + which, &kv_full[s]);
-          };
-          if (k) copy(p, dst, page, 0);
-          if (v) copy(p - kLag, dst + kTB, WIDE ? page1 : page2, 1);
-        }
-        page2 = page1;
-        page1 = page;
-        page = next;
-      }
-    }
-    if (lane == 0) {   // every copy must have landed before the CTA exits, also where another role gave up
-      volatile int never = 0;
-      for (uint32_t i = count > kS ? count - kS : 0; i < count; ++i)
-        mbar_wait(&kv_full[i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
-    }
-    __syncwarp();
-  } else if (warp == kQWarp) {
-    // ------------------------------------------------ copies of Q: a box is a row tile, 64 elements wide
-    if (lane == 0) {
-      constexpr int kHalves = DP / 64, kTiles = WIDE ? 2 : 1;
-      constexpr uint32_t kQBufs = WIDE ? 1 : 2;
-      const uint32_t bytes = uint32_t(r.tile_tokens * r.group) * 128u * kHalves * kTiles;
-      uint32_t items = 0;
-      for (; w.more(); w.next(c, r), ++items) {
-        const uint32_t qb = items % kQBufs, use = items / kQBufs;
-        if (!wait(&q_free[qb], use + 1, kErrQ)) break;
-        mbar_expect_tx(&q_full[qb], bytes);
-        const int tok = w.s.row0 + w.tile * tokens;
-#pragma unroll
-        for (int x = 0; x < kHalves * kTiles; ++x) {
-          const int h = x % kHalves, t = x / kHalves;
-          tma_load_3d(su32(base + S::kQ + (qb + t) * kTB + h * kTile * 128), &map_q, 64 * h, w.head * r.group,
-                      tok + t * r.tile_tokens, &q_full[qb]);
-        }
-      }
-      volatile int never = 0;   // the last fill of each buffer
-      for (uint32_t i = items > kQBufs ? items - kQBufs : 0; i < items; ++i)
-        mbar_wait(&q_full[i % kQBufs], (i / kQBufs) & 1, &never, kErrDrain, &g_attn_error);
-    }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------ MMA issue
-    // Event e of a piece is stream e & 1's tile e / 2, key tile e / 2 (wide) or e (narrow): the scores of
-    // the first two events, then per event its second product and the scores of the event after next
-    // (the same stream's next tile, which may overwrite the weights just used: MMAs run in order).
-    if (elect_one()) {
-      const uint32_t tmem = *tmem_base;
-      const int bf = kF16 ? 0 : 1;
-      const uint32_t id_s = idesc_f16(bf, kTile, kTile), id_o = idesc_f16(bf, kTile, ksteps * 16) | kTransposeB;
-      const uint64_t q_desc = sw128_desc(su32(base + S::kQ)), k_desc = sw128_desc(su32(base + S::kRing)),
-                     v0_desc = v_desc(su32(base + S::kRing + kTB));
-      // barriers by their shared-memory addresses
-      const uint32_t bars = su32(bar), b_kv_full = bars + 4 * 8, b_kv_free = b_kv_full + kS * 8, b_s_full = b_kv_free + kS * 8,
-                     b_p_ready = b_s_full + 16, b_o_full = b_p_ready + 16, b_o_free = b_o_full + 16;
-      auto wait_at = [&](uint32_t b, uint32_t parity, int code) {
-        return mbar_wait_at(b, parity & 1, abort_flag, code, &g_attn_error);
-      };
-      uint32_t items = 0, stage = 0, use = 0;   // the ring's present stage and its use's parity
-      uint32_t phases = 0;   // bit st: p_ready, bit 2 + st: o_free (an array would live in local memory)
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------ copies: a lane per page of a tile
+      const int ps = c.page_size(), per = ps < kTile ? kTile / ps : 1, box = min(ps, kTile);
+      const int halves = DP / 64;
+      uint32_t count = 0;
       bool ok = true;
-      for (; ok && w.more(); w.next(c, r), ++items) {
-        const int qb = WIDE ? 0 : items & 1;
-        const int n0 = w.stream_tiles(r, WIDE, 0), n1 = w.stream_tiles(r, WIDE, 1);
-        const int events = WIDE ? 2 * w.cnt : w.cnt;
-        ok = wait(&q_full[qb], WIDE ? items : items >> 1, kErrQ);
-        const uint64_t q0 = q_desc + uint64_t(qb * (kTB >> 4)), q1 = q0 + uint64_t(WIDE ? kTB >> 4 : 0);
-        // i: the stream's tile; st is a constant in every copy of these (an index into registers)
-        auto scores = [&](int st, int i) {
-          if (i < (st ? n1 : n0)) {
-            mma_scores<DP / 16>(tmem + st * kTile, st ? q1 : q0, k_desc + uint64_t(stage * (2 * kTB >> 4)), id_s, ksteps);
-            tc_commit_at(b_s_full + st * 8);
-          }
+      for (; ok && w.more(); next_item()) {
+        const int cnt = w.cnt, t0 = w.t0, keys = w.s.keys, head = w.head;
+        const int32_t *tab = c.table + int64_t(w.s.slot) * c.max_pages;
+        // page of this lane's part of key tile j; c.pages (outside the map: reads as zero) past the keys
+        auto page_of = [&](int j) -> int {
+          const int key = (t0 + j) * kTile + lane * ps;
+          if (j >= cnt || lane >= per || key >= keys) return c.pages;
+          const int p = __ldg(tab + (key >> c.page_shift));
+          if (p >= 0 && p < c.pages) return p;
+          if (MOE_CHECKED) check_fail(kCheckPage);
+          return c.pages;
         };
-        auto output = [&](int st, int i) -> bool {
-          const int n = st ? n1 : n0;
-          if (i < n) {
-            if (i == 0 && !wait_at(b_o_free + st * 8, (phases >> (2 + st)) ^ 1, kErrO)) return false;
-            if (!wait_at(b_p_ready + st * 8, phases >> st, kErrP)) return false;
-            phases ^= 1u << st;
-            tc_fence_after();
-            mma_output(tmem + 2 * kTile + st * DP, tmem + st * kTile, v0_desc + uint64_t(stage * (2 * kTB >> 4)), id_o, i != 0);
-            if (i + 1 == n) {
-              tc_commit_at(b_o_full + st * 8);
-              phases ^= 4u << st;
-            }
-          }
-          return true;
-        };
-#pragma unroll 1   // the loop shares the instruction cache with the softmax: twice its size measured 9% slower
-        for (int i = -1; ok && 2 * i < events; ++i) {
+        int page = page_of(0), page1 = c.pages, page2 = c.pages;   // of key tiles p, p - 1, p - 2
+        for (int p = 0; p < cnt + kLag; ++p, ++count) {
+          const uint32_t s = count % kS;
+          const int next = page_of(p + 1);
+          if (!(ok = wait_warp(&kv_free[s], count / kS + 1, kErrKv))) break;
+          const bool k = p < cnt, v = p >= kLag;
+          if (lane == 0) mbar_expect_tx(&kv_full[s], (k ? kTB : 0) + (v ? kTB : 0));
+          __syncwarp();
+          if (lane < per) {
+            const uint32_t dst = su32(base + S::kRing + s * 2 * kTB) + lane * box * 128;
+            auto copy = [&](int j, uint32_t to, int pg, int which) {
+              const int slot = ((t0 + j) * kTile) & (ps - 1);   // nonzero in 256-token pages only
 #pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const int e = 2 * i + st;
-            if (!ok || e >= events) break;
-            if (!WIDE || st == 0) {
-              if (!(ok = wait_at(b_kv_full + stage * 8, use, kErrKv))) break;
+              for (int h = 0; h < halves; ++h)
+                tma_load_4d(to + h * kTile * 128, &map_kv, 64 * h, slot, head, 2 * pg + which, &kv_full[s]);
+            };
+            if (k) copy(p, dst, page, 0);
+            if (v) copy(p - kLag, dst + kTB, WIDE ? page1 : page2, 1);
+          }
+          page2 = page1;
+          page1 = page;
+          page = next;
+        }
+      }
+      if (lane == 0) {   // every copy must have landed before the CTA exits, also where another role gave up
+        volatile int never = 0;
+        for (uint32_t i = count > kS ? count - kS : 0; i < count; ++i)
+          mbar_wait(&kv_full[i % kS], (i / kS) & 1, &never, kErrDrain, &g_attn_error);
+      }
+      __syncwarp();
+    } else if (warp == kQWarp) {
+      // ------------------------------------------------ copies of Q: a box is a row tile, 64 elements wide
+      if (lane == 0) {
+        constexpr int kHalves = DP / 64, kTiles = WIDE ? 2 : 1;
+        constexpr uint32_t kQBufs = WIDE ? 1 : 2;
+        const uint32_t bytes = uint32_t(r.tile_tokens * r.group) * 128u * kHalves * kTiles;
+        uint32_t items = 0;
+        for (; w.more(); w.next(c, r), ++items) {
+          const uint32_t qb = items % kQBufs, use = items / kQBufs;
+          if (!wait(&q_free[qb], use + 1, kErrQ)) break;
+          mbar_expect_tx(&q_full[qb], bytes);
+          const int tok = w.s.row0 + w.tile * tokens;
+#pragma unroll
+          for (int x = 0; x < kHalves * kTiles; ++x) {
+            const int h = x % kHalves, t = x / kHalves;
+            tma_load_3d(su32(base + S::kQ + (qb + t) * kTB + h * kTile * 128), &map_q, 64 * h, w.head * r.group,
+                        tok + t * r.tile_tokens, &q_full[qb]);
+          }
+        }
+        volatile int never = 0;   // the last fill of each buffer
+        for (uint32_t i = items > kQBufs ? items - kQBufs : 0; i < items; ++i)
+          mbar_wait(&q_full[i % kQBufs], (i / kQBufs) & 1, &never, kErrDrain, &g_attn_error);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------ MMA issue
+      // Event e of a piece is stream e & 1's tile e / 2, key tile e / 2 (wide) or e (narrow): the scores of
+      // the first two events, then per event its second product and the scores of the event after next
+      // (the same stream's next tile, which may overwrite the weights just used: MMAs run in order).
+      if (elect_one()) {
+        const uint32_t tmem = *tmem_base;
+        const int bf = kF16 ? 0 : 1;
+        const uint32_t id_s = idesc_f16(bf, kTile, kTile), id_o = idesc_f16(bf, kTile, ksteps * 16) | kTransposeB;
+        const uint64_t q_desc = sw128_desc(su32(base + S::kQ)), k_desc = sw128_desc(su32(base + S::kRing)),
+                       v0_desc = v_desc(su32(base + S::kRing + kTB));
+        // barriers by their shared-memory addresses
+        const uint32_t bars = su32(bar), b_kv_full = bars + 4 * 8, b_kv_free = b_kv_full + kS * 8, b_s_full = b_kv_free + kS * 8,
+                       b_p_ready = b_s_full + 16, b_o_full = b_p_ready + 16, b_o_free = b_o_full + 16;
+        auto wait_at = [&](uint32_t b, uint32_t parity, int code) {
+          return mbar_wait_at(b, parity & 1, abort_flag, code, &g_attn_error);
+        };
+        uint32_t items = 0, stage = 0, use = 0;   // the ring's present stage and its use's parity
+        uint32_t phases = 0;   // bit st: p_ready, bit 2 + st: o_free (an array would live in local memory)
+        bool ok = true;
+        for (; ok && w.more(); w.next(c, r), ++items) {
+          const int qb = WIDE ? 0 : items & 1;
+          const int n0 = w.stream_tiles(r, WIDE, 0), n1 = w.stream_tiles(r, WIDE, 1);
+          const int events = WIDE ? 2 * w.cnt : w.cnt;
+          ok = wait(&q_full[qb], WIDE ? items : items >> 1, kErrQ);
+          const uint64_t q0 = q_desc + uint64_t(qb * (kTB >> 4)), q1 = q0 + uint64_t(WIDE ? kTB >> 4 : 0);
+          // i: the stream's tile; st is a constant in every copy of these (an index into registers)
+          auto scores = [&](int st, int i) {
+            if (i < (st ? n1 : n0)) {
+              mma_scores<DP / 16>(tmem + st * kTile, st ? q1 : q0, k_desc + uint64_t(stage * (2 * kTB >> 4)), id_s, ksteps);
+              tc_commit_at(b_s_full + st * 8);
+            }
+          };
+          auto output = [&](int st, int i) -> bool {
+            const int n = st ? n1 : n0;
+            if (i < n) {
+              if (i == 0 && !wait_at(b_o_free + st * 8, (phases >> (2 + st)) ^ 1, kErrO)) return false;
+              if (!wait_at(b_p_ready + st * 8, phases >> st, kErrP)) return false;
+              phases ^= 1u << st;
               tc_fence_after();
+              mma_output(tmem + 2 * kTile + st * DP, tmem + st * kTile, v0_desc + uint64_t(stage * (2 * kTB >> 4)), id_o, i != 0);
+              if (i + 1 == n) {
+                tc_commit_at(b_o_full + st * 8);
+                phases ^= 4u << st;
+              }
             }
-            if (i >= 0 && !(ok = output(st, i))) break;
-            if (e + 2 < events) {
-              scores(st, i + 1);
-              if (e + 3 == events) tc_commit(&q_free[qb]);   // the item's last scores: Q may be replaced
-            }
-            if (!WIDE || st == 1) {
-              tc_commit_at(b_kv_free + stage * 8);
-              stage = stage + 1 == kS ? 0 : stage + 1;
-              use ^= stage == 0 ? 1 : 0;
+            return true;
+          };
+#pragma unroll 1   // the loop shares the instruction cache with the softmax: twice its size measured 9% slower
+          for (int i = -1; ok && 2 * i < events; ++i) {
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+              const int e = 2 * i + st;
+              if (!ok || e >= events) break;
+              if (!WIDE || st == 0) {
+                if (!(ok = wait_at(b_kv_full + stage * 8, use, kErrKv))) break;
+                tc_fence_after();
+              }
+              if (i >= 0 && !(ok = output(st, i))) break;
+              if (e + 2 < events) {
+                scores(st, i + 1);
+                if (e + 3 == events) tc_commit(&q_free[qb]);   // the item's last scores: Q may be replaced
+              }
+              if (!WIDE || st == 1) {
+                tc_commit_at(b_kv_free + stage * 8);
+                stage = stage + 1 == kS ? 0 : stage + 1;
+                use ^= stage == 0 ? 1 : 0;
+              }
             }
           }
         }
+        tc_commit(drain);
+        volatile int never = 0;
+        mbar_wait(drain, 0, &never, kErrDrain, &g_attn_error);
       }
-      tc_commit(drain);
-      volatile int never = 0;
-      mbar_wait(drain, 0, &never, kErrDrain, &g_attn_error);
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
     // ------------------------------------------------ softmax and epilogue
@@ -822,8 +829,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i) {
         const int j = WIDE ? i : 2 * i + st, tile = t0 + j;
-        if (!(ok = wait(&s_full[st], ns, kErrS))) break;
-        __syncwarp();
+        if (!(ok = wait_warp(&s_full[st], ns, kErrS))) break;
         ++ns;
         tc_fence_after();
         if (work) {
@@ -907,7 +913,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // tokens (0 x NaN would reach every row); rows that do see those get them added in the epilogue
           constexpr uint32_t kExp = (kF16 ? 0x7C00u : 0x7F80u) * 0x10001u, kLow = (kF16 ? 0x0400u : 0x0080u) * 0x10001u;
           const uint32_t vi = copies + j + kLag;
-          if (!(ok = wait(&kv_full[vi % kS], vi / kS, kErrKv))) break;
+          if (!(ok = wait_warp(&kv_full[vi % kS], vi / kS, kErrKv))) break;
           const int key = tile * kTile + row;   // this thread's row of the V tile
           if (key >= start) {
 #pragma unroll 1
@@ -948,7 +954,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int n1 = WIDE ? 0 : w.cnt >> 1;
       if constexpr (WIDE) {
         if (n > 0) {
-          if (!(ok = wait(&o_full[st], no[0], kErrO))) break;
+          if (!(ok = wait_warp(&o_full[st], no[0], kErrO))) break;
           ++no[0];
         }
       } else {
@@ -958,7 +964,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mine[st * kTile] = make_float2(ref, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&x_full[q4]);
-        if (!(ok = wait(&x_full[q4], nx, kErrX))) break;
+        if (!(ok = wait_warp(&x_full[q4], nx, kErrX))) break;
         ++nx;
         const float2 b = mine[(st ^ 1) * kTile];
         const float top = fmaxf(ref, b.x);
@@ -967,10 +973,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         f1 = st == 0 ? fo : fm;
         l = st == 0 ? l * f0 + b.y * f1 : b.y * f0 + l * f1;   // the same sum in both warps
         ref = top;
-        if (!(ok = wait(&o_full[0], no[0], kErrO))) break;
+        if (!(ok = wait_warp(&o_full[0], no[0], kErrO))) break;
         ++no[0];
         if (n1 > 0) {
-          if (!(ok = wait(&o_full[1], no[1], kErrO))) break;
+          if (!(ok = wait_warp(&o_full[1], no[1], kErrO))) break;
           ++no[1];
         }
       }
