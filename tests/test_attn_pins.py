@@ -189,3 +189,16 @@ def test_attention_refuses_bad_arguments(L):
     assert go(T=0) == 0 and go(n=0) == 0
     assert L.moe_tree_mask(P, P, P, 1, 4, 0, P, P, NUL) == -1 and L.moe_tree_mask(P, P, NUL, 1, 4, 1, P, P, NUL) == -1
     assert L.moe_tree_mask(NUL, P, P, 1, 4, 1, P, P, NUL) == -1 and L.moe_tree_mask(NUL, NUL, NUL, 0, 4, 1, NUL, NUL, NUL) == 0
+
+
+def test_binding_refuses_wrong_tensors():
+    """Host tensors, wrong types and shapes are refused before the library is asked."""
+    from weight_only_int4_route_gb300 import attn
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    x, tab = torch.zeros((2, 1, 16)), torch.zeros((4, 16))
+    with pytest.raises(AssertionError):
+        attn.rope(x, i32(0, 1), tab)
+    with pytest.raises(AssertionError):
+        attn.KVCache(torch.zeros((1, 4, 2, 1, 8, 16), dtype=torch.bfloat16), i32(-1, -1).reshape(2, 1), i32(0, 0), i32(0, 0, 0, 0))
+    with pytest.raises(AssertionError):
+        attn.tree_mask(i32(-1), i32(0, 1), i32(0), 1)

@@ -201,3 +201,21 @@ def test_offsets_past_32_bits(attn):
     assert torch.equal(cache.pool[:, P - 4 + 101 // ps, 0, :, 101 % ps], k[:, 199])
     cache.copy(i32([P - 3]), i32([P - 1]))
     assert torch.equal(cache.pool[:, P - 1], cache.pool[:, P - 3])
+
+
+def test_binding_refuses_wrong_tensors(attn):
+    cache, _ = make(attn)
+    k = torch.zeros((2, 2, 16), dtype=torch.bfloat16, device=DEV)
+    ok = dict(cu=i32([0, 2]), seqs=i32([0]), start=i32([0]))
+    for bad in (dict(k=k.float()), dict(k=k.cpu()), dict(k=k[:, :1]), dict(k=k, cu=i32([0])), dict(k=k, seqs=i32([0]).long()),
+                dict(k=k, start=i32([0]).cpu()), dict(k=k, layer=None), dict(k=k.transpose(1, 2).contiguous().transpose(1, 2))):
+        a = {**ok, **bad}
+        with pytest.raises(AssertionError):
+            cache.append(a["k"], a["k"], a["cu"], a["seqs"], a["start"], layer=a.get("layer", 0))
+    with pytest.raises(AssertionError):
+        cache.extend(i32([0]), i32([1, 2]))
+    with pytest.raises(AssertionError):
+        attn.attention(k.reshape(2, 2, 16), cache, i32([0, 2, 3]), i32([0]), i32([0]))
+    from weight_only_int4_route_gb300 import moe
+    with pytest.raises(moe.MoeError):
+        cache.append(k, k, **ok, layer=2)

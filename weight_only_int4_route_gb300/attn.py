@@ -31,9 +31,14 @@ def _stream(t: torch.Tensor) -> int:
     return _raw_stream(t.get_device())
 
 
+def _on_gpu(*tensors) -> None:
+    for t in tensors:
+        assert t.is_cuda, "tensors are on the GPU"
+
+
 def _ints(*tensors) -> None:
     for t in tensors:
-        assert t.dtype is _i32 and t.is_contiguous(), "index tensors are contiguous int32"
+        assert t.is_cuda and t.dtype is _i32 and t.is_contiguous(), "index tensors are contiguous int32 on the GPU"
 
 
 def _scratch(nbytes: int, like: torch.Tensor) -> torch.Tensor:
@@ -61,6 +66,7 @@ def rope(x: torch.Tensor, pos: torch.Tensor, cos_sin: torch.Tensor, interleaved:
     ot, oh, o1 = out.stride()
     if T == 1:
         xt = ot = H * D                                # torch leaves the stride of a dimension of one open
+    _on_gpu(x, out, cos_sin)
     assert x1 == 1 and o1 == 1 and out.shape == x.shape and out.dtype == x.dtype
     assert pos.numel() == T and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()
     n_pos, rot = cos_sin.shape
@@ -77,6 +83,7 @@ class KVCache:
         L, P, two, H, ps, D = pool.shape
         S, W = table.shape
         _ints(table, lens, refs)
+        _on_gpu(pool)
         assert two == 2 and pool.is_contiguous() and lens.numel() == S and refs.numel() == P
         self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
         self.layers, self.kv_heads, self.head_dim = L, H, D
@@ -147,14 +154,17 @@ class KVCache:
             L, kl, vl = 1, 0, 0
         T = shape[-3]
         kt, vt = (ks[-3], vs[-3]) if T != 1 else (H * D, H * D)
+        _on_gpu(k, v)
         assert start.numel() == n and cu.numel() == n + 1 and v.shape == shape and shape[-2:] == (H, D)
         assert k.dtype == v.dtype == self.pool.dtype and ks[-2:] == vs[-2:] == (D, 1)
         out, rope_args, q_args = None, (None, None, 0, 0, 0), (None, 0, 0, None)
         if cos_sin is not None:
             _ints(pos)
+            _on_gpu(cos_sin)
             assert pos.numel() == T and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()
             rope_args = (cos_sin.data_ptr(), pos.data_ptr(), *cos_sin.shape, int(interleaved))
         if q is not None:
+            _on_gpu(q)
             qs, qh = q.stride(), q.shape[1]
             assert q.shape == (T, qh, D) and qs[1:] == (D, 1) and q.dtype == k.dtype
             out = torch.empty((T, qh, D), dtype=q.dtype, device=q.device)
@@ -187,6 +197,7 @@ def attention(q: torch.Tensor, cache: KVCache, cu: torch.Tensor, seqs: torch.Ten
     qt, qh, q1 = q.stride()
     _ints(cu, seqs, start)
     n = seqs.numel()
+    _on_gpu(q)
     assert start.numel() == n and cu.numel() == n + 1
     assert D == cache.head_dim and q.dtype == cache.pool.dtype and (qh == D or H == 1) and q1 == 1
     words, bits = 0, None
