@@ -203,6 +203,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device: torch.device):
+    """torch's current stream on `device`, which has to be the current GPU: the library launches there, whatever the stream."""
+    assert device.index is None or device.index == torch._C._cuda_getDevice(), "tensors are on the current GPU"
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
