@@ -528,7 +528,8 @@ int moe_kv_append(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, int6
  * q_heads * head_dim), heads contiguous; out: contiguous; lse: fp32 (T, q_heads) or NULL.  head_dim
  * <= 128 here, q_heads % kv_heads == 0, q_heads / kv_heads <= 128.  Rows of no sequence are left as
  * they were.  Two launches; the result does not depend on the workspace's contents and is the same
- * on every run.
+ * on every run.  A workspace of moe_attention_workspace_size(desc, T, n, q_heads) bytes serves every call of
+ * at most T tokens with the same desc and q_heads, of however many sequences.
  * moe_tree_mask: parents int32 (T), parents[r] = index within its sequence of row r's parent
  *   (smaller than its own), -1 = the context; anything else makes row r and its descendants padding.
  *   mask row: the token and its ancestors; pos[r] (may be NULL) = start[i] + depth (start[i] for

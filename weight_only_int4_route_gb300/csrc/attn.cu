@@ -1269,11 +1269,12 @@ struct AttnPlan {
 };
 // Two row tiles per item when a sequence brings more rows than one tile holds on average: then
 // both streams share every key tile; with fewer rows the second row tile would be padding.
-AttnPlan plan_attention(const moe_kv_desc *d, int64_t T, int64_t n, int64_t q_heads) {
+bool wide_form(const moe_kv_desc *d, int64_t T, int64_t n, int64_t q_heads) { return T * (q_heads / d->kv_heads) > n * kTile; }
+AttnPlan plan_attention(const moe_kv_desc *d, bool wide) {
   AttnPlan p{};
   p.grid = num_sms();
   p.dp = d->head_dim <= 64 ? 64 : 128;
-  p.wide = T * (q_heads / d->kv_heads) > n * kTile;
+  p.wide = wide;
   const size_t rows = size_t(2 * p.grid) * (p.wide ? 2 : 1) * kTile;
   p.o_ml = align256(size_t(2 * p.grid) * sizeof(Piece));
   p.o_o = p.o_ml + align256(rows * sizeof(float2));
@@ -1358,7 +1359,7 @@ int check_attention(const moe_kv_desc *d, int64_t T, int64_t n, int64_t q_heads)
 
 extern "C" size_t moe_attention_workspace_size(const moe_kv_desc *desc, int64_t T, int64_t n, int64_t q_heads) {
   if (check_attention(desc, T, n, q_heads) != MOE_OK || T == 0 || n == 0) return 0;
-  return plan_attention(desc, T, n, q_heads).bytes;
+  return plan_attention(desc, wide_form(desc, T, 1, q_heads)).bytes;   // as many tokens of one sequence need the most
 }
 
 extern "C" int moe_attention(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, const void *q,
@@ -1379,7 +1380,7 @@ extern "C" int moe_attention(const moe_kv_desc *desc, const moe_kv *kv, int64_t 
   MOE_REQUIRE(aligned16(q) && aligned16(cu) && aligned16(seqs) && aligned16(start) && aligned16(mask) && aligned16(out) &&
                   aligned16(lse),
               "pointers must be 16-byte aligned");
-  const AttnPlan pl = plan_attention(desc, T, n, q_heads);
+  const AttnPlan pl = plan_attention(desc, wide_form(desc, T, n, q_heads));
   MOE_REQUIRE(workspace && aligned16(workspace), "workspace must be non-null and 16-byte aligned");
   if (workspace_bytes < pl.bytes)
     return set_error(MOE_ERR_WORKSPACE, "attention workspace %zu < %zu bytes", workspace_bytes, pl.bytes);
