@@ -521,7 +521,8 @@ int moe_kv_append(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, int6
  *   32 * mask_words on are visible to no row.  A row without any bit is padding and sees nothing.
  * Positions from max_pages * page_size on are in no cache and visible to no row; the rows of a
  * sequence whose slot does not exist or whose start is negative or past that see nothing.  A row that
- * sees nothing (or whose scores are all -inf) gets out = 0 and lse = -inf.  What the cache holds where
+ * sees nothing (or whose scores are all -inf) gets out = 0 and lse = -inf; one with a score of +inf gets out = NaN
+ * (inf / inf) and lse = inf, one with a score of NaN gets NaN in both.  What the cache holds where
  * a row does not look has no influence on it, NaN and infinities included.  Sums and softmax
  * statistics are fp32; the weights are rounded to dtype for their product with V.
  * q: (T, q_heads, head_dim) of the cache's dtype, token stride given (a multiple of 8, at least

@@ -42,6 +42,7 @@
 // Every wait is bounded (see mbar_wait); when one expires the CTA records a code, drains its own copies
 // and MMAs, frees its tensor memory and returns.
 #include <atomic>
+#include <cfloat>
 #include <climits>
 
 #include "kv_internal.cuh"
@@ -891,8 +892,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
             for (int y = 0; y < 4; ++y) top[y] = max3(top[y], v[x + 2 * y], v[x + 2 * y + 1]);
           }
-          const float mt = max3(max3(top[0], top[1], v[kTile - 1]), max3(top[2], v[kTile - 4], v[kTile - 3]),
-                                fmaxf(top[3], v[kTile - 2])) * r.scale_log2;
+          float mt = max3(max3(top[0], top[1], v[kTile - 1]), max3(top[2], v[kTile - 4], v[kTile - 3]),
+                          fmaxf(top[3], v[kTile - 2])) * r.scale_log2;
+          if (mt > FLT_MAX) mt = FLT_MAX;   // a score of +inf: its weight is inf, not inf - inf, and so are the sum and lse
           const bool grow = i == 0 ? mt > m : mt > m + kLazy || (m == -INFINITY && mt > m);
           if (i > 0 && __any_sync(0xffffffffu, grow)) {
             // the products that have been added to O are complete: this tile's scores were issued behind them
