@@ -122,3 +122,21 @@ def test_a_rotary_table_on_another_gpu_is_refused(calls, monkeypatch):
     with pytest.raises(AssertionError):
         attn.rope_table(2, 2)
     assert not calls
+
+
+def odd(t):
+    """t with a stride of 5 in every dimension of one."""
+    return t.as_strided(t.shape, [5 if n == 1 else s for n, s in zip(t.shape, t.stride())])
+
+
+@pytest.mark.parametrize("name", ["rope", "rope_out", "append_rotated", "attention"])
+def test_the_stride_of_a_single_head_is_open(calls, name):
+    s = setup(heads=1)
+    CALLS[name](s)
+    plain = list(calls)
+    s.x = odd(s.x)
+    calls.clear()
+    CALLS[name](s)
+    strides = {"moe_rope": slice(3, 7)}
+    for (n0, a0), (n1, a1) in zip(plain, calls):
+        assert n0 == n1 and a0[strides.get(n0, slice(0))] == a1[strides.get(n0, slice(0))]

@@ -79,6 +79,8 @@ def rope(x: torch.Tensor, pos: torch.Tensor, cos_sin: torch.Tensor, interleaved:
     ot, oh, o1 = out.stride()
     if T == 1:
         xt = ot = H * D                                # torch leaves the stride of a dimension of one open
+    if H == 1:
+        xh = oh = D
     assert x1 == 1 and o1 == 1 and out.shape == x.shape and out.dtype == x.dtype
     assert pos.numel() == T and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()
     n_pos, rot = cos_sin.shape
@@ -170,6 +172,8 @@ class KVCache:
         if layer is None:
             assert len(shape) == 4 and shape[0] == self.layers
             layer, L, kl, vl = 0, self.layers, ks[0], vs[0]
+            if L == 1:
+                kl = vl = 0                                # torch leaves the stride of a dimension of one open
         else:
             assert len(shape) == 3
             L, kl, vl = 1, 0, 0
@@ -177,7 +181,7 @@ class KVCache:
         kt, vt = (ks[-3], vs[-3]) if T != 1 else (H * D, H * D)
         _on(dev, k, v)
         assert start.numel() == n and cu.numel() == n + 1 and v.shape == shape and shape[-2:] == (H, D)
-        assert k.dtype == v.dtype == self.pool.dtype and ks[-2:] == vs[-2:] == (D, 1)
+        assert k.dtype == v.dtype == self.pool.dtype and ks[-1] == vs[-1] == 1 and (H == 1 or ks[-2] == vs[-2] == D)
         out, rope_args, q_args = None, (None, None, 0, 0, 0), (None, 0, 0, None)
         if cos_sin is not None:
             _ints(dev, pos)
@@ -187,7 +191,7 @@ class KVCache:
         if q is not None:
             _on(dev, q)
             qs, qh = q.stride(), q.shape[1]
-            assert q.shape == (T, qh, D) and qs[1:] == (D, 1) and q.dtype == k.dtype
+            assert q.shape == (T, qh, D) and qs[2] == 1 and (qh == 1 or qs[1] == D) and q.dtype == k.dtype
             out = torch.empty((T, qh, D), dtype=q.dtype, device=q.device)
             q_args = (q.data_ptr(), qs[0] if T != 1 else qh * D, qh, out.data_ptr())
         r = KvRows(k.data_ptr(), v.data_ptr(), kt, kl, vt, vl, cu.data_ptr(), seqs.data_ptr(), start.data_ptr(), n, T,
