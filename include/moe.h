@@ -462,9 +462,9 @@ int moe_rope(const void *x, int dtype, int64_t T, int64_t heads, int64_t head_di
  *   ascending offsets from start[i]; the j-th is moved to offset j (K and V, every layer), the
  *   length becomes start[i] + their number, and pages past it are released.  No entries: roll back to
  *   start[i].  A sequence is skipped if start[i] is negative or the new length would exceed the
- *   present one; entries out of order or past the length move nothing.  The tokens from start[i]
- *   on must be the sequence's own: not shared by a fork made since they were written (with
- *   entries that move; a roll back is always possible).
+ *   present one; an entry that is not above the one before it, or past the length, moves nothing.  The
+ *   tokens from start[i] on must be the sequence's own: not shared by a fork made since they were
+ *   written (with entries that move; a roll back is always possible).
  * moe_kv_free: release the sequences' pages; their slots are empty afterwards.
  * moe_kv_copy: page src[i] -> page dst[i], every layer; no page may be both a source and a
  *   destination or twice a destination.  Ids outside [0, pages) are skipped.

@@ -282,7 +282,8 @@ __device__ void move_tokens(const KvView &c, const Kept &k, const int32_t *__res
       int64_t f = -1, t = -1;
       if (j < n) {
         const int from = keep[k.k0 + j0 + j];
-        if (from > j0 + j && from < k.len - k.start) {
+        const bool ascends = j0 + j == 0 || from > keep[k.k0 + j0 + j - 1];
+        if (ascends && from > j0 + j && from < k.len - k.start) {
           auto at = [&](int pos) -> int64_t {
             const int p = valid_page(c, tab[pos >> c.page_shift]);
             return p < 0 ? -1 : (int64_t(p) * 2 * c.kv_heads * ps + (pos & (ps - 1))) * c.head_dim;
