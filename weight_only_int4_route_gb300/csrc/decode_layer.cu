@@ -36,12 +36,11 @@
 // Every wait is bounded (about a second); on expiry a code goes to this file's device error
 // word, an abort flag makes every other wait give up, and the launch returns with incomplete
 // outputs (moe_device_error reports it).
-#include <cuda.h>
-
 #include <algorithm>
 #include <cmath>
 
 #include "moe_internal.cuh"
+#include "tensor_map.cuh"
 
 namespace moe {
 
@@ -923,24 +922,6 @@ __global__ void __launch_bounds__(kThr, 1) decode_layer_kernel(const __grid_cons
     for (int rc = lane; rc < P.rcmax; rc += 32) ctrl[cFc1 + kLine * rc] = 0;
     fence_acq_rel();
   }
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
-  return fn;
 }
 
 // 4-bit codes (rows of K/8 words): 32-word (two chunks) x 64-row boxes, 128-byte swizzle.
