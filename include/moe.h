@@ -514,7 +514,8 @@ int moe_kv_append(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, int6
  * Attention over the cache.  n sequences; the rows cu[i] .. cu[i+1] of q are sequence seqs[i]'s new
  * tokens, already in the cache at positions start[i] on.  Query head h reads K/V head h / (q_heads /
  * kv_heads).  For a row and head, over its visible keys j:
- *   s_j = scale * q . k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = ln sum_j exp(s_j).
+ *   s_j = scale * q . k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = ln sum_j exp(s_j),
+ *   0 < scale <= 2.3e38.
  * mask NULL (prompts, causal): new token t sees positions 0 .. start[i] + t.
  * mask uint32 (T, mask_words) (a tree of drafted tokens): bit j of row r (word j / 32, bit j % 32)
  *   makes new token j of the same sequence visible, and all positions before start[i] are; tokens from

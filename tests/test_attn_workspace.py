@@ -1,4 +1,5 @@
-"""A workspace of moe_attention_workspace_size serves every call of fewer tokens or sequences (host side only)."""
+"""moe_attention on the host side: a workspace of moe_attention_workspace_size serves every call of fewer tokens or
+sequences; the range of the scale."""
 import ctypes
 
 import pytest
@@ -25,3 +26,13 @@ def test_fewer_tokens_or_sequences_need_no_more(L, head_dim, kv_heads, group):
                 for n2 in (1, 2, 3, 64, 1000):
                     assert size(T2, n2) <= size(T, n), (T, n, T2, n2)
     assert size(0, 1) == 0 and size(1, 0) == 0
+
+
+def test_scales_that_leave_the_range_are_refused(L):
+    """Scores are taken to base 2: scale * log2(e) has to be finite too.  Nothing to do (T = 0), but the arguments are checked."""
+    d, p, P = M.KvDesc(1, 64, 16, 4, 64, 8, 8, M.BF16), M.KvPointers(*[0x1000] * 4), ctypes.c_void_p(0x1000)
+
+    def go(scale):
+        return L.moe_attention(ctypes.byref(d), ctypes.byref(p), 0, P, 512, 8, 0, P, P, P, 1, None, 0, scale, P, None, P, 1 << 30, None)
+    assert go(2.3e38) == 0 and go(1e-30) == 0
+    assert go(2.4e38) == -1 and go(3e38) == -1 and go(-1.0) == -1

@@ -1391,7 +1391,8 @@ extern "C" int moe_attention(const moe_kv_desc *desc, const moe_kv *kv, int64_t 
               "q's token stride must be a multiple of 8 that holds the heads (%lld)", (long long)q_token_stride);
   MOE_REQUIRE(mask == nullptr || (mask_words >= 1 && mask_words <= 1024), "need 1 <= mask_words <= 1024 (%lld)",
               (long long)mask_words);
-  MOE_REQUIRE(scale > 0.f && scale <= 3.0e38f, "scale must be positive and finite");
+  // times log2(e) it has to be finite still: a score of 0 would be 0 x inf
+  MOE_REQUIRE(scale > 0.f && scale <= 2.3e38f, "scale must be positive, at most 2.3e38 (%g)", double(scale));
   if (T == 0 || n == 0) return MOE_OK;
   MOE_REQUIRE(q && cu && seqs && start && out, "null pointer argument");
   MOE_REQUIRE(aligned16(q) && aligned16(cu) && aligned16(seqs) && aligned16(start) && aligned16(mask) && aligned16(out) &&
