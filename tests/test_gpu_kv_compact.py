@@ -21,7 +21,7 @@ def moves(ref, q, start, keep):
     ref._cut(q, start + len(keep))
 
 
-# one launch (16-byte pieces of a token's rows in all layers at most 2048), and a launch for the moves
+# few 16-byte pieces of a token's rows in all layers (16): one launch; many (2560): one for the moves
 SHAPES = [dict(layers=2, H=2, D=16), dict(layers=20, H=4, D=128)]
 
 
