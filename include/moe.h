@@ -535,7 +535,8 @@ int moe_kv_append(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, int6
  * moe_tree_mask: parents int32 (T), parents[r] = index within its sequence of row r's parent
  *   (smaller than its own), -1 = the context; anything else makes row r and its descendants padding.
  *   mask row: the token and its ancestors; pos[r] (may be NULL) = start[i] + depth (start[i] for
- *   padding).  At most 32 * mask_words tokens of a sequence; later ones become padding.
+ *   padding).  At most 32 * mask_words tokens of a sequence; later ones become padding.  Rows of no
+ *   sequence are left as they were.
  * ------------------------------------------------------------------------------------ */
 int moe_tree_mask(const int32_t *parents, const int32_t *cu, const int32_t *start, int64_t n, int64_t T,
                   int64_t mask_words, uint32_t *mask, int32_t *pos, moe_stream_t stream);

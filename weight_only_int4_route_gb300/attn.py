@@ -10,6 +10,8 @@ tensors are all on the current GPU; others are refused.
     q = cache.append(k, v, cu, seqs, start, layer, q=q, pos=pos, cos_sin=table)
     out = attention(q, cache, cu, seqs, start, mask=mask, layer=layer)
     cache.compact(seqs, start, cu_keep, keep)               # keep the accepted path
+
+A kernel that gives up on one of its bounded waits leaves its outputs incomplete and says so through moe.device_error.
 """
 from __future__ import annotations
 
@@ -202,7 +204,8 @@ class KVCache:
 
 def tree_mask(parents: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, max_draft: int):
     """Trees of drafted tokens, given by each token's parent within its sequence (-1: the context) -> (mask, pos):
-    each token's visible drafted tokens as bits, int32 (T, ceil(max_draft / 32)), and its position."""
+    each token's visible drafted tokens as bits, int32 (T, ceil(max_draft / 32)), and its position.  Rows of no sequence are
+    not written."""
     dev = _device(parents)
     _ints(dev, parents, cu, start)
     T, words = parents.numel(), max(1, -(-max_draft // 32))
@@ -218,7 +221,8 @@ def attention(q: torch.Tensor, cache: KVCache, cu: torch.Tensor, seqs: torch.Ten
               mask: Optional[torch.Tensor] = None, layer: int = 0, scale: Optional[float] = None,
               return_lse: bool = False):
     """Attention of the new tokens q (T, q_heads, head_dim), already in the cache from start[i] on: causal, or with
-    `mask` (tree_mask) over drafted trees.  Returns out, or (out, lse) with lse fp32 (T, q_heads)."""
+    `mask` (tree_mask) over drafted trees.  Returns out, or (out, lse) with lse fp32 (T, q_heads); rows of no sequence
+    (before cu[0], from cu[-1] on) are not written."""
     T, H, D = q.shape
     qt, qh, q1 = q.stride()
     dev = _device(cache.pool)

@@ -27,17 +27,24 @@
 // S0 S1 (128 columns each, the weights replace the scores' first 64), outputs O0 O1 (head_dim columns
 // each): all 512 columns at head_dim 128, so a stream's next scores wait for its second product.
 //
-// Measured on GB300 (bf16, 32 query and 8 K/V heads of 128 unless said):
-//   prompt of 8191 tokens             375 us, 1465 TFLOP/s of visible pairs (0.76 of the measured matrix peak)
-//   6 prompts of 1 to 2500 tokens     216 us, 1105 TFLOP/s
-//   32 trees of 8-32 tokens over 500-8000 cached ones   106 us, 5.2 TB/s
-//   5 trees over 30000-150000 cached tokens, f16, 16 and 8 heads of 64   157 us, 5.9 TB/s
-//   one token over 1000, 16 heads     12 us for both kernels, all of it latency
+// Measured on GB300 (bf16, 32 query and 8 K/V heads of 128 unless said), calls in a row:
+//   prompt of 8191 tokens             400 us, 1372 TFLOP/s of visible pairs (0.71 of the measured matrix peak), the
+//                                     power cap active; 376 us, 1462 TFLOP/s (0.76) in runs too short for it
+//   6 prompts of 1 to 2500 tokens     217 us, 1099 TFLOP/s (0.57)
+//   32 trees of 8-32 tokens over 500-8000 cached ones   106 us, 5.2 TB/s (0.77 of the measured copy rate)
+//   5 trees over 30000-150000 cached tokens, f16, 16 and 8 heads of 64   157 us, 6.0 TB/s (0.88)
+//   one token over 1000, 16 heads     15 us from a graph (9 + 3 us in the two kernels), all of it latency
 // What bounds the wide form: the chain scores -> softmax -> weights -> product of a stream takes about 2500
 // cycles, the MMAs of both streams 2050 of them; without any softmax the same loop takes 367 us.  The
 // MMA thread's waits and the instruction cache (its loop beside the softmax's) make up the rest.  The narrow
 // form reads each K and V once (DRAM bytes = the cache's), at 6.3 TB/s between a start of 4 us (finding the
 // work, first pages) and the slowest CTA's end, up to 8% after the mean.
+//
+// Precision: scores, maxima, sums and the output accumulator are fp32; the weights are rounded to the cache's type,
+// because a product of 16-bit values takes both operands of one type and V is of that type.  Their error is one
+// rounding of each weight: 0.0022 of the output's norm against 64 bits in bf16 (0.00028 in f16), where the output's own
+// rounding is 0.0017 (0.0002).  Weights in two 16-bit parts bring it down to that, with two second products: 181 instead
+// of 157 us for the trees over long contexts.  The sums take the weights as they are before, and lse is exact to fp32.
 //
 // Every wait is bounded (see mbar_wait); when one expires the CTA records a code, drains its own copies
 // and MMAs, frees its tensor memory and returns.
@@ -86,8 +93,13 @@ constexpr float kLazy = 8.f;
 // looked at in vain adds nothing.
 constexpr int kBadTiles = 64;
 // What an item costs beside its key tiles (its queries, its first tiles' latency, its epilogue), in key
-// tiles: shares are dealt with it counted in.  Not in calls so small that every key tile gets a CTA
-// of its own (up to kSmallUnits units per CTA): there the longest share decides.
+// tiles: shares are dealt with it counted in.  With 0, 2, 4 and 8 tiles: prompt of 8191 tokens 667, 443, 378 and 393 us;
+// 6 prompts of 1 to 2500 338, 232, 214 and 222; 64 of 200 131, 119, 120 and 120; 32 trees of 8-32 115, 107, 106 and 107;
+// 300 single tokens over 300 271, 271, 258 and 249; 5 trees over long contexts 155 to 156 with any.
+// Not in calls so small that every key tile gets a CTA of its own (up to kSmallUnits units per CTA): there the longest
+// share decides.  8 single tokens over 400: 16.9 us without the cost, 18.0 with it; prompt of 700 tokens,
+// 16 heads of 64: 17.4 and 18.4.  From there on it turns: prompt of 1000 tokens 42.4 and 32.6, 16 single tokens over 1000
+// and 16 heads 41.1 and 38.2.
 constexpr int kItemCost = 4, kSmallUnits = 4;
 enum : int { kErrQ = 11, kErrKv = 12, kErrS = 13, kErrP = 14, kErrO = 15, kErrX = 16, kErrDrain = 17 };
 
@@ -1285,7 +1297,11 @@ struct AttnPlan {
   size_t o_ml, o_o, bytes;
 };
 // Two row tiles per item when a sequence brings more rows than one tile holds on average: then
-// both streams share every key tile; with fewer rows the second row tile would be padding.
+// both streams share every key tile; with fewer rows the second row tile would be padding.  One and two row tiles, 32 query
+// and 8 K/V heads of 128: 64 single tokens over 2000 99 and 110 us; 32 trees over 4000 of 32 tokens (128 rows) 104 and 113,
+// of 33 185 and 119, of 64 188 and 129; 32 prompts of 40 29 and 23; 4 prompts of 500 38 and 35.  The average misjudges
+// two row tiles over few keys (8 times 64 tokens over 1000: 29 and 33) and mixtures: a prompt of 2000 beside 32 single
+// tokens over 4000 takes 125 and 135 (two are chosen), one of 600 beside 20 takes 72 and 78 (one is).
 bool wide_form(const moe_kv_desc *d, int64_t T, int64_t n, int64_t q_heads) { return T * (q_heads / d->kv_heads) > n * kTile; }
 AttnPlan plan_attention(const moe_kv_desc *d, bool wide) {
   AttnPlan p{};

@@ -8,7 +8,8 @@
 // Bookkeeping is latency (a few dependent reads per call), data is bandwidth.  Measured on GB300: 104 pages of
 // 16 layers copied (872 MB moved) in 129 us, 6.8 TB/s; 405 new tokens of 24 sequences
 // written to 32 layers (106 MB) in 18.5 us, 5.7 TB/s, and the accepted ones moved up (31 MB) in 9 us;
-// extend 7 us, the page side of a compaction 4 us.
+// the page side of a compaction 4 us; extend of 8 sequences 4.4 us where the free pages are found among the first 1000,
+// 5.7 and 21.5 us where they are the last of 10^4 and 10^5 (one block looks at 4096 pages a round).
 #include "kv_internal.cuh"
 
 namespace moe {

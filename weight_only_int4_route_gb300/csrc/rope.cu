@@ -132,9 +132,11 @@ extern "C" int moe_rope(const void *x, int dtype, int64_t T, int64_t heads, int6
   // in place the untouched part needs no visit
   const int units = x == out ? turned : rope_units(V, int(head_dim), int(rot), interleaved);
   // several heads a thread (128 bytes of loads: a unit of the half layout is two vectors, of the interleaved one a
-  // single one) once that leaves every SM half a load of threads; fewer threads than that would wait for
-  // memory with too little in flight, and more would spend themselves on indices (one head a thread: 45 us
-  // instead of 28 on 8192 x 32 heads of f16, interleaved)
+  // single one) once that leaves every SM half a load of threads; with fewer threads too little is in flight, with more
+  // they spend themselves on indices.  Several and one, from a graph, 32 heads of 128 in bf16: 128 tokens 3.1 and 2.6 us in
+  // either layout, 1024 4.1 and 4.6 (interleaved, half of the head 4.6 and 5.2), 4096 8.2 and 11.3 (10.2 and 15.9), 16384
+  // 42 and 48 (48 and 60); 16 heads in f32 within 8 % from 512 tokens on, interleaved 4096 7.7 and 12.8.  They are even at
+  // a fifth to a third of this bound: what lies between pays up to 2.5 us (a cache append of 48 heads 4).
   const bool many = T * heads * units >= int64_t(num_sms()) * 1024 * (interleaved ? 8 : 4);
   auto typed = [&](auto zero) -> int {
     using E = decltype(zero);
