@@ -35,8 +35,9 @@ def test_another_gpu_is_refused(calls):
 
     ids = torch.zeros((1, 2, 2), dtype=torch.int32).as_subclass(Fake)
     counts = torch.zeros((1, 4), dtype=torch.int32).as_subclass(Fake)
+    layer = types.SimpleNamespace(max_T=4, p=types.SimpleNamespace(w1=counts))
     for call in (lambda: moe.device_error("cuda:1"), lambda: moe.check_status("cuda:1"),
-                 lambda: moe.elb_accumulate(ids, 4, counts)):
+                 lambda: moe.elb_accumulate(ids, 4, counts), lambda: moe.LayerGraph(layer, 1)):
         with pytest.raises(AssertionError):
             call()
     assert not calls

@@ -202,9 +202,13 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(device: torch.device):
-    """torch's current stream on `device`, which has to be the current GPU: the library launches there, whatever the stream."""
+def _on_current(device: torch.device):
+    """The library launches on the current GPU, whatever the stream: a call's tensors have to be there."""
     assert device.index is None or device.index == torch._C._cuda_getDevice(), "tensors are on the current GPU"
+
+
+def _stream(device: torch.device):
+    _on_current(device)
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
@@ -438,6 +442,7 @@ class LayerGraph:
     def __init__(self, layer: "Layer", T: int):
         assert 0 < T <= layer.max_T
         dev = layer.p.w1.device
+        _on_current(dev)
         self.layer, self.T = layer, T
         self.x = torch.zeros((T, layer.cfg.d), dtype=layer.cfg.torch_dtype, device=dev)
         self.out = torch.empty((T, layer.cfg.d), dtype=layer.cfg.torch_dtype, device=dev)
