@@ -546,6 +546,61 @@ int moe_attention(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, cons
                   const uint32_t *mask, int64_t mask_words, float scale, void *out, float *lse, void *workspace,
                   size_t workspace_bytes, moe_stream_t stream);
 
+/* ====================================================================================
+ * The dense operators around experts and attention: norm of the residual stream, products of
+ * 8-bit integers for the projections, log probabilities of the logits.  [Specter] background on GPTQ keeps
+ * attention and the shared expert in 16 bits; these calls are for models that hold those projections in 8 bits too.  The pages
+ * define no kernel for them; the formulas below are the definition.  Same conventions as above, except that x,
+ * residual, sum, logits, a, w and out may start on any element and have any stride of at least a row's length (16-byte
+ * starts and strides are faster).  The stride of a single row is not looked at.  Strides are in elements.
+ *
+ * moe_rmsnorm: h = x + residual (fp32; residual NULL: h = x),
+ *   sum = RN(h),   v = h / sqrt(mean(h^2) + eps) * weight (weight NULL: ones),   y = RN(v),
+ *   q = round(v * 127 / max|v|), ties to even, q_scale = max|v| / 127, so that v is about q * q_scale.
+ * fp32 throughout, each output rounded once from it (h is not rounded before it is normalised).  sum, y and (q, q_scale) are
+ * each written unless NULL.  A row of zeros gets q = 0 and q_scale = 0; one that holds a NaN or an infinity, or whose values
+ * times weight pass fp32, gets q = 0 and q_scale = NaN, so that every product with it is NaN (y follows the
+ * formula).  x, residual, weight, sum, y: dtype F16 | BF16 | F32; q: int8 (T, d); q_scale: fp32 (T); y and q contiguous.
+ * 1 <= d <= 16384, eps >= 0.  sum may be x or residual itself with the same stride (in place); outputs must not overlap
+ * inputs or each other otherwise.
+ * moe_quantize_rows: q and q_scale of v = x, d <= 16384.
+ * ------------------------------------------------------------------------------------ */
+int moe_rmsnorm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, const void *weight,
+                int dtype, int64_t T, int64_t d, float eps, void *sum, int64_t sum_stride, void *y, int8_t *q,
+                float *q_scale, moe_stream_t stream);
+int moe_quantize_rows(const void *x, int64_t x_stride, int dtype, int64_t T, int64_t d, int8_t *q, float *q_scale,
+                      moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Product of 8-bit integers with a scale for each row of a (token) and each row of w (output channel):
+ *   acc = sum_k a[m, k] * w[n, k]   (exact, 32-bit),
+ *   out[m, n] = RN((fp32(acc) * a_scale[m]) * w_scale[n] (+ bias[n]))   (fp32 operations in this order, each rounded).
+ * a: int8 (M, K), w: int8 (N, K) (moe_quantize_rows gives either; every int8 value is taken), a_scale fp32 (M), w_scale
+ * fp32 (N), bias fp32 (N) or NULL, out (M, N) F16 | BF16 | F32.  1 <= K <= 131071.  The result does not depend on M, on the
+ * other rows or on which kernel runs: a token's outputs are the same bits alone and in any batch.
+ * workspace: >= moe_linear_w8a8_workspace_size(M, N, K) bytes; one sized for M serves every call of fewer rows with the same N
+ * and K.  Its contents have no influence.  Rows of w that do not all start on 16 bytes (K % 16 != 0 among them) are copied into it
+ * on every call. */
+size_t moe_linear_w8a8_workspace_size(int64_t M, int64_t N, int64_t K);
+int moe_linear_w8a8(const int8_t *a, int64_t a_stride, const float *a_scale, const int8_t *w, int64_t w_stride,
+                    const float *w_scale, const float *bias, int64_t M, int64_t N, int64_t K, void *out,
+                    int64_t out_stride, int out_dtype, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Log probabilities under softmax(scale * logits) of a row: of given tokens, of the most probable ones, and the entropy.
+ *   lse[t] = ln sum_j exp(scale x[t, j]),   logprob[t, i] = scale x[t, ids[t, i]] - lse[t],
+ *   entropy[t] = -sum_j p_j ln p_j (terms with p_j = 0 are 0),   p_j = exp(scale x[t, j] - lse[t]),
+ *   top_ids[t, :] = the k largest logits, descending, equal logits -> lower id; top_logprob[t, :] theirs.
+ * logits: (T, V) F16 | BF16 | F32; ids: int32 (T, n_ids), ids outside [0, V) get NaN; all else fp32 or int32,
+ * contiguous; entropy and lse may be NULL.  scale > 0 (a temperature's inverse), 0 <= k <= 64, T < 2^27, V < 2^30.  fp32 sums
+ * relative to the row's largest logit; results are the same on every run.
+ * Masked logits (-inf) have probability 0 and log probability -inf; they come last among the alternatives.  A row of nothing
+ * but -inf gets lse = -inf, log probabilities of -inf and entropy 0.  Places past V get id -1 and -inf.  A row with a NaN gets NaN
+ * everywhere and ids of -1.  A row with a +inf gets lse = inf, entropy NaN, -inf for finite logits and NaN for infinite ones. */
+int moe_token_logprobs(const void *logits, int64_t stride, int dtype, int64_t T, int64_t V, float scale,
+                       const int32_t *ids, int64_t n_ids, float *logprob, float *entropy, float *lse, int k,
+                       int32_t *top_ids, float *top_logprob, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

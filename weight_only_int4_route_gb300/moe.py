@@ -121,6 +121,13 @@ _SIGS = {
     "moe_attention_workspace_size": (_c_size, [_KD, _c_i64, _c_i64, _c_i64]),
     "moe_attention": (_c_int, [_KD, _KP, _c_i64, _vp, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _c_i64, _vp, _c_i64,
                                ctypes.c_float, _vp, _vp, _vp, _c_size, _vp]),
+    "moe_rmsnorm": (_c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _c_int, _c_i64, _c_i64, ctypes.c_float, _vp, _c_i64, _vp, _vp, _vp, _vp]),
+    "moe_quantize_rows": (_c_int, [_vp, _c_i64, _c_int, _c_i64, _c_i64, _vp, _vp, _vp]),
+    "moe_linear_w8a8_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "moe_linear_w8a8": (_c_int, [_vp, _c_i64, _vp, _vp, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _vp, _c_i64, _c_int, _vp,
+                                 _c_size, _vp]),
+    "moe_token_logprobs": (_c_int, [_vp, _c_i64, _c_int, _c_i64, _c_i64, ctypes.c_float, _vp, _c_i64, _vp, _vp, _vp, _c_int, _vp,
+                                    _vp, _vp]),
 }
 
 # stage boundaries recorded by moe_layer_forward_profiled (enum in include/moe.h)
