@@ -144,7 +144,7 @@ def linear(a=P, ar=16, sa=P, w=P, wr=16, sw=P, b=P, M=3, N=5, K=16, o=P, orow=5,
     ("null", ARG, dict(w=None)), ("null", ARG, dict(sw=None)), ("null", ARG, dict(o=None)), ("16-byte", ARG, dict(sa=0x1004)),
     ("16-byte", ARG, dict(b=0x1004)), ("start on an element", ARG, dict(o=ODD)), ("workspace", WORKSPACE, dict(K=15, wb=79)),
     ("workspace", WORKSPACE, dict(wr=17, wb=0)), ("workspace", WORKSPACE, dict(w=ODD, wb=0)), ("workspace", ARG, dict(K=15, ws=None)),
-    ("workspace", ARG, dict(K=15, ws=0x1008))])
+    ("workspace", ARG, dict(K=15, ws=0x1008)), ("workspace", WORKSPACE, dict(M=100, wb=0)), ("workspace", ARG, dict(M=100, ws=None))])
 def test_linear_refusals(built, why, status, args):
     assert linear(**args) == status and why in moe.lib().moe_last_error_string().decode()
 

@@ -8,6 +8,7 @@
 #include <cmath>
 
 #include "kv_internal.cuh"
+#include "linear8.cuh"
 
 namespace moe {
 
@@ -274,6 +275,7 @@ extern "C" int moe_device_error(moe_stream_t stream, int32_t *host_code) {
   MOE_TRY(read_device_error(reinterpret_cast<cudaStream_t>(stream), &v));
   MOE_TRY(decode_error_take(&v));
   MOE_TRY(attn_error_take(&v));
+  MOE_TRY(linear8_error_take(&v));
   *host_code = v;
   return MOE_OK;
 }

@@ -143,40 +143,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity, volatile
   return moe::mbar_wait<CL>(b, parity, abort_flag, code, &g_moe_device_error);
 }
 
-// The eight MMAs of one 128-wide K block (A from tensor memory), in one statement: the first
-// accumulates only when `acc` is set, the others always; MMA j reads A columns a + 8j and the
-// B descriptor advanced by j's start offset (16-byte units: 2 per 16-wide step inside a 64-wide
-// swizzle atom column, half16 to the next column block).  The offsets are added to the low word
-// only: the start-address field cannot carry (shared addresses stay below 256 KB).
-#define MOE_TC_MMA_KBLOCK(GROUP)                                                                                  \
-  asm volatile(                                                                                                   \
-      "{\n .reg .pred p, t;\n .reg .b32 a1, bl1;\n .reg .b64 bd;\n"                                            \
-      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, %5, %5;\n"                                                       \
-      " mov.b64 bd, {%2, %3};\n tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], [%1], bd, %4, p;\n"             \
-      " add.u32 a1, %1, 8;\n add.u32 bl1, %2, 2;\n mov.b64 bd, {bl1, %3};\n"                                  \
-      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], [a1], bd, %4, t;\n"                                     \
-      " add.u32 a1, %1, 16;\n add.u32 bl1, %2, 4;\n mov.b64 bd, {bl1, %3};\n"                                 \
-      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], [a1], bd, %4, t;\n"                                     \
-      " add.u32 a1, %1, 24;\n add.u32 bl1, %2, 6;\n mov.b64 bd, {bl1, %3};\n"                                 \
-      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], [a1], bd, %4, t;\n"                                     \
-      " add.u32 a1, %1, 32;\n add.u32 bl1, %2, %6;\n mov.b64 bd, {bl1, %3};\n"                                \
-      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], [a1], bd, %4, t;\n"                                     \
-      " add.u32 a1, %1, 40;\n add.u32 bl1, %2, %7;\n mov.b64 bd, {bl1, %3};\n"                                \
-      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], [a1], bd, %4, t;\n"                                     \
-      " add.u32 a1, %1, 48;\n add.u32 bl1, %2, %8;\n mov.b64 bd, {bl1, %3};\n"                                \
-      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], [a1], bd, %4, t;\n"                                     \
-      " add.u32 a1, %1, 56;\n add.u32 bl1, %2, %9;\n mov.b64 bd, {bl1, %3};\n"                                \
-      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], [a1], bd, %4, t;\n"                                     \
-      "}\n" ::"r"(d), "r"(a), "r"(bl), "r"(bh), "r"(idesc), "r"(acc), "n"(HALF16), "n"(HALF16 + 2), "n"(HALF16 + 4), \
-      "n"(HALF16 + 6)                                                                                             \
-      : "memory")
-template <int HALF16, bool PAIR>
-__device__ __forceinline__ void tc_mma_kblock_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  const uint32_t bl = uint32_t(b), bh = uint32_t(b >> 32);
-  if constexpr (PAIR) MOE_TC_MMA_KBLOCK("2");   // M = 256: A rows and B columns from both CTAs of the pair
-  else MOE_TC_MMA_KBLOCK("1");
-}
-#undef MOE_TC_MMA_KBLOCK
 template <typename T> __device__ __forceinline__ float ldscale(const uint16_t *s, int64_t i) {
   const uint16_t b = s[i];
   if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(b));

@@ -5,29 +5,11 @@
 // same bits.
 #include <algorithm>
 
+#include "linear8.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
-
-struct LinearArgs {
-  const int8_t *a, *w;
-  const float *a_scale, *w_scale, *bias;
-  void *out;
-  int64_t M, a_stride, w_stride, out_stride;   // strides in elements (= bytes for a and w)
-  int N, K;       // K as given; w's rows hold K rounded up to 16, zeros past K
-  int out_dtype;
-};
-
-__device__ __forceinline__ float scaled(int acc, float sa, float sw, const float *bias, int n) {
-  const float v = __fmul_rn(__fmul_rn(float(acc), sa), sw);
-  return bias ? __fadd_rn(v, bias[n]) : v;
-}
-__device__ __forceinline__ void store_out(void *out, int dtype, int64_t at, float v) {
-  if (dtype == MOE_F32) static_cast<float *>(out)[at] = v;
-  else if (dtype == MOE_F16) static_cast<__half *>(out)[at] = from_f32<__half>(v);
-  else static_cast<__nv_bfloat16 *>(out)[at] = from_f32<__nv_bfloat16>(v);
-}
 
 // Rows of K bytes -> rows of `pitch` bytes, zeros behind: weights whose rows do not start on 16 bytes.
 __global__ void __launch_bounds__(256) pad_rows_kernel(const int8_t *w, int64_t stride, int64_t rows, int K, int pitch, int8_t *out) {
@@ -162,7 +144,7 @@ __global__ void __launch_bounds__(kStreamThreads) linear8_stream_kernel(const Li
   for (int i = tid; i < 16 * rows; i += kStreamThreads) {
     const int r = i >> 4, n = n0 + (i & 15);
     if (n < p.N)
-      store_out(p.out, p.out_dtype, (m0 + r) * p.out_stride + n, scaled(s_sum[r][i & 15], p.a_scale[m0 + r], p.w_scale[n], p.bias, n));
+      store_out(p.out, p.out_dtype, (m0 + r) * p.out_stride + n, scaled(s_sum[r][i & 15], p.a_scale[m0 + r], p.w_scale[n], p.bias != nullptr, p.bias ? p.bias[n] : 0.f));
   }
 }
 
@@ -199,6 +181,11 @@ template <int MT> int launch_stream(const LinearArgs &p, cudaStream_t st) {
   return check_launch("linear_w8a8");
 }
 
+// Rows up to which the weights are streamed past all of them at once.
+constexpr int64_t kStreamRows = 32;
+
+// The workspace: the weights' rows padded to 16 bytes (used if they need it), then the rows as f16 (many rows).
+size_t padded_bytes(int64_t N, int64_t K) { return align256(size_t(N) * size_t((K + 15) & ~int64_t(15))); }
 bool needs_padding(const int8_t *w, int64_t w_stride, int64_t K) { return K % 16 != 0 || w_stride % 16 != 0 || !aligned16(w); }
 
 int check_sizes(int64_t M, int64_t N, int64_t K) {
@@ -214,7 +201,7 @@ using namespace moe;
 
 extern "C" size_t moe_linear_w8a8_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (check_sizes(M, N, K) != MOE_OK) return 0;
-  return align256(size_t(N) * size_t((K + 15) & ~int64_t(15)));
+  return padded_bytes(N, K) + (M > kStreamRows ? linear8_tc_rows_bytes(M, K) : 0);
 }
 
 extern "C" int moe_linear_w8a8(const int8_t *a, int64_t a_stride, const float *a_scale, const int8_t *w, int64_t w_stride,
@@ -229,20 +216,24 @@ extern "C" int moe_linear_w8a8(const int8_t *a, int64_t a_stride, const float *a
   MOE_REQUIRE((reinterpret_cast<uintptr_t>(out) & (dtype_size(out_dtype) - 1)) == 0, "out must start on an element");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   LinearArgs p{a, w, a_scale, w_scale, bias, out, M, a_stride, w_stride, out_stride, int(N), int(K), out_dtype};
-  if (needs_padding(w, N == 1 ? 16 : w_stride, K)) {
-    const int pitch = int((K + 15) & ~int64_t(15));
-    if (workspace_bytes < size_t(N) * pitch)
-      return set_error(MOE_ERR_WORKSPACE, "linear_w8a8 workspace %zu < %zu bytes", workspace_bytes, size_t(N) * pitch);
+  if (N == 1) p.w_stride = (K + 15) & ~int64_t(15);   // a single row's is not looked at
+  const bool pad = needs_padding(w, p.w_stride, K), many = M > kStreamRows;
+  const size_t need = (pad || many ? padded_bytes(N, K) : 0) + (many ? linear8_tc_rows_bytes(M, K) : 0);
+  if (need > 0) {
+    if (workspace_bytes < need) return set_error(MOE_ERR_WORKSPACE, "linear_w8a8 workspace %zu < %zu bytes", workspace_bytes, need);
     MOE_REQUIRE(workspace && aligned16(workspace), "workspace must be non-null and 16-byte aligned");
+  }
+  if (pad) {
+    const int pitch = int((K + 15) & ~int64_t(15));
     int8_t *padded = static_cast<int8_t *>(workspace);
     const int64_t blocks = std::min<int64_t>(cdiv(N * pitch, 256), int64_t(num_sms()) * 32);
-    launch_pdl(pad_rows_kernel, dim3(unsigned(blocks)), dim3(256), 0, st, w, w_stride, N, int(K), pitch, padded);
+    launch_pdl(pad_rows_kernel, dim3(unsigned(blocks)), dim3(256), 0, st, w, p.w_stride, N, int(K), pitch, padded);
     MOE_TRY(check_launch("linear_w8a8 padding"));
     p.w = padded;
     p.w_stride = pitch;
   }
+  if (many) return launch_linear8_tc(p, static_cast<char *>(workspace) + padded_bytes(N, K), st);
   if (M <= 8) return launch_stream<1>(p, st);
   if (M <= 16) return launch_stream<2>(p, st);
-  MOE_SUPPORT(cdiv(M, 32) <= 65535, "M too large");
   return launch_stream<4>(p, st);
 }
