@@ -67,8 +67,9 @@ def token_logprobs(x, ids, k, scale=1.0):
             if m > 0:
                 lp[z == m] = math.nan
         else:
-            lse[t] = m + math.log(float((z - m).exp().sum()))
-            lp = z - lse[t]
+            total = math.log(float((z - m).exp().sum()))
+            lse[t] = m + total
+            lp = (z - m) - total                       # rows of a type's lowest value: m + ln V has lost ln V
             entropy[t] = -sum(math.exp(v) * v for v in lp.tolist() if v > -800)
         for i in range(n):
             j = int(ids[t, i])

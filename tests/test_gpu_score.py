@@ -39,6 +39,7 @@ def check(dense, x, ids, k, scale=1.0):
 
     def near(got, ref, extra):
         got = got.double().cpu().reshape(ref.shape)
+        ref = torch.where(ref.abs() > torch.finfo(torch.float32).max * (1 + E), ref.sign() * math.inf, ref)   # past fp32
         assert torch.equal(torch.isnan(got), torch.isnan(ref))
         fine = torch.isfinite(ref)
         assert torch.equal(got[~fine & ~torch.isnan(ref)], ref[~fine & ~torch.isnan(ref)])
@@ -74,7 +75,8 @@ def test_scores(dense, dtype, T, V, k, pad):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T", [2, 800])
-@pytest.mark.parametrize("kind", ["equal", "zeros", "steps", "rising", "falling", "masked", "one_group", "peaked"])
+@pytest.mark.parametrize("kind", ["equal", "zeros", "steps", "rising", "falling", "masked", "one_group", "peaked", "lowest", "some_lowest",
+                                  "few_lanes"])
 def test_ties_and_orders(dense, dtype, T, kind):
     """Rows where many logits are equal, sorted rows, rows mostly masked, rows where nearly every logit is above the best one of
     a few threads (the k best are then found one after the other)."""
@@ -83,7 +85,11 @@ def test_ties_and_orders(dense, dtype, T, kind):
     g = torch.Generator().manual_seed(3)
     row = {"equal": torch.full((V,), 1.5), "zeros": torch.where(j % 2 == 0, -0.0, 0.0), "steps": (j * 7919 % 5),
            "rising": j / 1000, "falling": -j / 1000, "masked": torch.where(j % 4001 == 3, j / 5000, -math.inf),
-           "peaked": torch.where(j == 77, 90.0, -20.0), "one_group": torch.randn(V, generator=g)}[kind]
+           "peaked": torch.where(j == 77, 90.0, -20.0), "one_group": torch.randn(V, generator=g),
+           "lowest": torch.full((V,), torch.finfo(dtype).min), "few_lanes": torch.randn(V, generator=g),
+           "some_lowest": torch.where(j % 1999 == 5, j / 5000, torch.finfo(dtype).min)}[kind]
+    if kind == "few_lanes":                                  # all large values are a few threads'
+        row = row + torch.where((j // (16 // torch.empty((), dtype=dtype).element_size())) % 256 < 14, 40.0, 0.0)
     if kind == "one_group":
         per = 16 // torch.empty((), dtype=dtype).element_size()
         row = row + torch.where((j // per) % 32 == 31, -30.0, 30.0)
@@ -97,8 +103,8 @@ def test_ties_and_orders(dense, dtype, T, kind):
     lp, h, lse, top, toplp = D.token_logprobs(x[few], ids[few][:, None], k)
     assert torch.equal(full.top_ids[few].cpu(), top)
     assert torch.equal(full.top_ids[2:], full.top_ids[:1].expand(T - 2, k))
-    assert torch.allclose(full.top_logprob[few].double().cpu(), toplp, rtol=0, atol=2e-4) and \
-        torch.allclose(full.lse[few].double().cpu(), lse, rtol=0, atol=2e-4)
+    assert torch.allclose(full.top_logprob[few].double().cpu(), toplp, rtol=1e-6, atol=2e-4) and \
+        torch.allclose(full.lse[few].double().cpu(), lse, rtol=1e-6, atol=2e-4)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -135,6 +141,22 @@ def test_ids_outside_the_vocabulary(dense):
 def test_scale(dense, scale):
     x, ids = draw(5, 3001, torch.float32)
     check(dense, x, ids, 9, scale)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [1e-30, 1e-5, 1.0, 30.0, 300.0])
+def test_masks_beside_the_lowest_values(dense, dtype, scale):
+    """-inf has no weight, however near the others are to the type's lowest value and however small the scale is."""
+    low = torch.finfo(dtype).min
+    x, ids = draw(6, 3000, dtype, 2, spread=1.0 if scale <= 1 else 0.01)
+    x[:, 1::3] = -math.inf
+    x[1, 0::3] = low
+    x[1, 2::3] = -math.inf                                   # a third at the lowest value, nothing else
+    x[2] = torch.where(torch.isfinite(x[2]), torch.full((), low, dtype=dtype), x[2])
+    x[2, 5] = low / 2
+    if dtype is not torch.float16 and scale <= 1:
+        x[3, 7], x[4, 8] = 3e38, 2.0 ** 101
+    check(dense, x, ids, 7, scale)
 
 
 def test_forms_of_ids(dense):

@@ -26,126 +26,164 @@ struct NormArgs {
 
 constexpr int kMaxD = 16384;
 
-template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
-  T v[V];
+// V elements of a row: 16 bytes, or one.  Words, not arrays of elements: those cost a permute for every element that is read
+// or put in (33 instructions an element in all, 9 now).
+template <typename T, int V> struct Pack {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const T *p) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+  __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]); }
+  __device__ __forceinline__ void widen(float (&f)[V]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        f[i] = __uint_as_float(w[i]);
+      } else if constexpr (std::is_same<T, __half>::value) {
+        const float2 two = __half22float2(u32_as_h2(w[i]));
+        f[2 * i] = two.x, f[2 * i + 1] = two.y;
+      } else {
+        f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+  __device__ __forceinline__ void narrow(const float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
+      else if constexpr (std::is_same<T, __half>::value) w[i] = h2_as_u32(__floats2half2_rn(f[2 * i], f[2 * i + 1]));
+      else w[i] = h2_as_u32(__floats2bfloat162_rn(f[2 * i], f[2 * i + 1]));
+    }
+  }
+  // the lowest bytes of the words
+  static __device__ __forceinline__ void store_codes(int8_t *p, const uint32_t (&c)[V]) {
+    uint32_t o[V / 4];
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+      o[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
+    if constexpr (V == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(o[0], o[1]);
+    else *reinterpret_cast<uint32_t *>(p) = o[0];
+  }
 };
-template <int V> struct alignas(V) Codes {
-  int8_t v[V];
+template <typename T> struct Pack<T, 1> {
+  T w;
+  __device__ __forceinline__ void load(const T *p) { w = *p; }
+  __device__ __forceinline__ void store(T *p) const { *p = w; }
+  __device__ __forceinline__ void widen(float (&f)[1]) const { f[0] = to_f32(w); }
+  __device__ __forceinline__ void narrow(const float (&f)[1]) { w = from_f32<T>(f[0]); }
+  static __device__ __forceinline__ void store_codes(int8_t *p, const uint32_t (&c)[1]) { *p = int8_t(c[0]); }
 };
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 
-// Row-wide sum and maximum (as the bits of a non-negative float, so that NaN and infinity are the largest).  Every thread
-// of the block takes part; the order of the additions is fixed.
-__device__ __forceinline__ void row_reduce(float &ss, uint32_t &top, int lanes, float (*s_sum)[32], uint32_t (*s_top)[32]) {
+// Row-wide sum and maximum (NaN if one is), in an order that depends on the row's size alone.  A row of 32 threads is a
+// warp's; a longer one is the block's, whose `turn`s use two places in turn, so that one barrier is enough.
+struct Exchange {
+  float sum[2][32], top[2][32];
+};
+__device__ __forceinline__ void row_reduce(float &ss, float &top, int lanes, Exchange &x, int &turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
   if (lanes == 32) return;
-  const int warp = threadIdx.x >> 5, n = lanes >> 5, first = warp / n * n;
-  __syncthreads();   // the exchange before this one has been read
+  const int warp = threadIdx.x >> 5, n = lanes >> 5;
   if ((threadIdx.x & 31) == 0) {
-    (*s_sum)[warp] = ss;
-    (*s_top)[warp] = top;
+    x.sum[turn][warp] = ss;
+    x.top[turn][warp] = top;
   }
   __syncthreads();
   ss = 0.f;
-  top = 0;
+  top = 0.f;
   for (int i = 0; i < n; ++i) {
-    ss += (*s_sum)[first + i];
-    top = max(top, (*s_top)[first + i]);
+    ss += x.sum[turn][i];
+    top = max_nan(top, x.top[turn][i]);
   }
+  turn ^= 1;
 }
 
-// Most threads of a block: what the registers of a thread's elements allow without spills.
-constexpr int most_threads(int V, int NV) { return V > 1 ? 1024 : (NV <= 8 ? 768 : 512); }
-
-// A row per `lanes` threads, NV vectors of V elements a thread; short rows share a block.  The weight is read again from
-// the L1 for the stores rather than kept in registers.
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(most_threads(V, NV)) norm_kernel(const NormArgs p) {
+// A row per `lanes` threads, NV vectors of V elements a thread; Q8: with 8-bit output.
+template <typename T, int V, int NV, int MOST, bool Q8>
+__global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs p) {
   pdl_enter();
-  __shared__ float s_sum[32];
-  __shared__ uint32_t s_top[32];
+  __shared__ Exchange exchange;
   using P = Pack<T, V>;
-  const int rows = blockDim.x / p.lanes, in = threadIdx.x / p.lanes, t = threadIdx.x - in * p.lanes;
-  const int64_t row = int64_t(blockIdx.x) * rows + in;
-  const int d = row < p.T ? p.d : 0;   // a row that is not there has no elements
+  const int rows = blockDim.x / p.lanes, t = int(threadIdx.x) % p.lanes;
+  const int64_t row = int64_t(blockIdx.x) * rows + int(threadIdx.x) / p.lanes;
+  if (row >= p.T) return;   // whole warps: no barrier is shared by several rows
+  auto at = [&](int i) { return (t + i * p.lanes) * V; };
   const T *x = static_cast<const T *>(p.x) + row * p.x_stride;
-  const T *residual = static_cast<const T *>(p.residual);
-  const T *weight = static_cast<const T *>(p.weight);
-  auto weight_of = [&](int at, int j) { return weight ? to_f32(weight[at + j]) : 1.f; };
+  P a[NV], b[NV], w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {   // what is not there is 0, a weight 1
+    float f[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = 0.f;
+    a[i].narrow(f);
+    b[i].narrow(f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = 1.f;
+    w[i].narrow(f);
+    if (at(i) < p.d) a[i].load(x + at(i));
+  }
+  if (p.residual) {
+    const T *y = static_cast<const T *>(p.residual) + row * p.residual_stride;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (at(i) < p.d) b[i].load(y + at(i));
+  }
+  if (p.weight) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (at(i) < p.d) w[i].load(static_cast<const T *>(p.weight) + at(i));
+  }
   float h[NV][V];
-  P a[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int at = (t + i * p.lanes) * V;
-    if (at < d) a[i] = *reinterpret_cast<const P *>(x + at);
+    float f[V];
+    a[i].widen(h[i]);
+    b[i].widen(f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) h[i][j] = 0.f;
-  }
-  if (residual) {
-    residual += row * p.residual_stride;
-    P b[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = (t + i * p.lanes) * V;
-      if (at < d) b[i] = *reinterpret_cast<const P *>(residual + at);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if ((t + i * p.lanes) * V < d) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[i][j] = to_f32(a[i].v[j]) + to_f32(b[i].v[j]);
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if ((t + i * p.lanes) * V < d) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[i][j] = to_f32(a[i].v[j]);
-      }
+    for (int j = 0; j < V; ++j) h[i][j] += f[j];
   }
   if (p.sum) {   // may be the residual or x itself: this thread's elements of both have been read
     T *s = static_cast<T *>(p.sum) + row * p.sum_stride;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int at = (t + i * p.lanes) * V;
-      if (at >= d) continue;
       P o;
-#pragma unroll
-      for (int j = 0; j < V; ++j) o.v[j] = from_f32<T>(h[i][j]);
-      *reinterpret_cast<P *>(s + at) = o;
+      o.narrow(h[i]);
+      if (at(i) < p.d) o.store(s + at(i));
     }
   }
-  float ss, eps = p.eps, r = 1.f;
-  uint32_t top;
-  auto reduce = [&]() {
-    ss = 0.f;
-    top = 0;
+  int turn = 0;
+  float ss, top, eps = p.eps, r = 1.f;
+  auto reduce = [&]() {   // elements that are not there are 0
+    ss = top = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int at = (t + i * p.lanes) * V;
-      if (at >= d) continue;
+      float f[V];
+      if (Q8) w[i].widen(f);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         ss = fmaf(h[i][j], h[i][j], ss);
-        if (p.q) top = max(top, __float_as_uint(fabsf(h[i][j] * weight_of(at, j))));
+        if (Q8) top = max_nan(top, fabsf(h[i][j] * f[j]));
       }
     }
-    row_reduce(ss, top, p.lanes, &s_sum, &s_top);
+    row_reduce(ss, top, p.lanes, exchange, turn);
   };
   reduce();
   if (p.norm) {
-    // squares past fp32 (magnitudes above 1.8e19): the row again, 2^-64 times as large.  A block's rows go round together.
-    if (__syncthreads_or(isinf(ss))) {
-      if (isinf(ss)) {
-        eps *= 0x1p-128f;
+    if (isinf(ss)) {   // squares past fp32 (magnitudes above 1.8e19): the row again, 2^-64 times as large
+      eps *= 0x1p-128f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int j = 0; j < V; ++j) h[i][j] *= 0x1p-64f;
-      }
+        for (int j = 0; j < V; ++j) h[i][j] *= 0x1p-64f;
       reduce();
     }
     r = rsqrtf(fmaf(ss, p.inv_d, eps));
@@ -154,53 +192,63 @@ __global__ void __launch_bounds__(most_threads(V, NV)) norm_kernel(const NormArg
     T *y = static_cast<T *>(p.y) + row * p.d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int at = (t + i * p.lanes) * V;
-      if (at >= d) continue;
-      P o;
+      float f[V];
+      w[i].widen(f);
 #pragma unroll
-      for (int j = 0; j < V; ++j) o.v[j] = from_f32<T>(h[i][j] * r * weight_of(at, j));
-      *reinterpret_cast<P *>(y + at) = o;
+      for (int j = 0; j < V; ++j) f[j] *= h[i][j] * r;
+      P o;
+      o.narrow(f);
+      if (at(i) < p.d) o.store(y + at(i));
     }
   }
-  if (p.q) {
-    const float m = __uint_as_float(top);
-    const bool fine = m <= 3.402823466e38f;   // neither infinite nor NaN
-    // 127 / m overflows below 2^-121: small rows are brought up first (exact)
-    const float up = m < 0x1p-60f ? 0x1p60f : 1.f;
-    const float step = m > 0.f && fine ? __fdiv_rn(127.f, m * up) : 0.f;
+  if (Q8) {
+    const bool fine = top <= 3.402823466e38f;   // neither infinite nor NaN
+    float step = 0.f, up = 1.f;
+    if (top > 0.f && fine) {
+      if (top < 0x1p-60f) {   // 127 / top overflows below 2^-121: small rows are brought up first (exact)
+        up = 0x1p60f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j) h[i][j] *= up;
+      }
+      step = __fdiv_rn(127.f, top * up);
+    }
     int8_t *q = p.q + row * p.d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int at = (t + i * p.lanes) * V;
-      if (at >= d) continue;
-      Codes<V> o;
+      float f[V];
+      w[i].widen(f);
+      uint32_t c[V];
+      // adding 1.5 * 2^23 rounds to whole numbers, ties to even, and leaves their low 8 bits in the lowest byte
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        o.v[j] = fine ? int8_t(__float2int_rn(h[i][j] * weight_of(at, j) * up * step)) : int8_t(0);
-      *reinterpret_cast<Codes<V> *>(q + at) = o;
+      for (int j = 0; j < V; ++j) c[j] = fine ? __float_as_uint(__fadd_rn(__fmul_rn(h[i][j] * f[j], step), 12582912.f)) : 0;
+      if (at(i) < p.d) P::store_codes(q + at(i), c);
     }
-    if (t == 0 && d > 0) p.scale[row] = fine ? __fdiv_rn(m, 127.f) * r : __int_as_float(0x7fc00000);
+    if (t == 0) p.scale[row] = fine ? __fdiv_rn(top, 127.f) * r : __int_as_float(0x7fc00000);
   }
 }
 
 template <typename T, int V> int launch_rows(NormArgs p, cudaStream_t st) {
   const int vecs = (p.d + V - 1) / V;
-  auto go = [&](auto nv) {
-    constexpr int NV = decltype(nv)::value;
+  auto go = [&](auto nv, auto most) {
+    constexpr int NV = decltype(nv)::value, MOST = decltype(most)::value;
     p.lanes = int(cdiv(cdiv(vecs, NV), 32) * 32);
-    // short rows share blocks of about 128 threads
-    const int rows = p.lanes >= 128 ? 1 : 128 / p.lanes;
-    launch_pdl(norm_kernel<T, V, NV>, dim3(unsigned(cdiv(p.T, rows))), dim3(unsigned(rows * p.lanes)), 0, st, p);
+    const int rows = p.lanes == 32 ? 4 : 1;
+    launch_pdl(p.q ? norm_kernel<T, V, NV, MOST, true> : norm_kernel<T, V, NV, MOST, false>, dim3(unsigned(cdiv(p.T, rows))),
+               dim3(unsigned(rows * p.lanes)), 0, st, p);
     return check_launch("rmsnorm");
   };
-  // 8 elements a thread for few rows of few elements (more threads, less latency), 16 otherwise; single elements
-  // (rows that do not start on 16 bytes) 8 or 32
-  if constexpr (V == 1) {
-    if (vecs <= 768 * 8) return go(std::integral_constant<int, 8>{});
-    return go(std::integral_constant<int, 32>{});
+  using std::integral_constant;
+  if constexpr (V == 1) {   // rows that do not start on 16 bytes
+    if (vecs <= 512 * 8) return go(integral_constant<int, 8>{}, integral_constant<int, 512>{});
+    return go(integral_constant<int, 32>{}, integral_constant<int, 512>{});
   } else {
-    if (vecs <= 1024 * (8 / V) && p.T < num_sms()) return go(std::integral_constant<int, 8 / V>{});
-    return go(std::integral_constant<int, 16 / V>{});
+    // 8 elements a thread for few rows (more threads, less latency), 32 (fp32: 16) otherwise
+    if (vecs <= 512 * (8 / V) && p.T < num_sms()) return go(integral_constant<int, 8 / V>{}, integral_constant<int, 512>{});
+    if (vecs <= 512 * 4) return go(integral_constant<int, 4>{}, integral_constant<int, 512>{});
+    if constexpr (V == 4) return go(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
+    return set_error(MOE_ERR_UNSUPPORTED, "rows of at most %d elements", kMaxD);
   }
 }
 

@@ -1,17 +1,19 @@
 // Log probabilities of given tokens, entropy and top alternatives of rows of logits.
 //
-// With z_j = scale * x_j, in powers of two (c = scale log2 e):
-//   lse = ln sum_j exp z_j,  logprob_t = z_t - lse,  entropy = lse - sum_j p_j z_j
-// One pass over the row: every thread keeps its largest logit m, the reference M = fl(m c), Z = sum 2^(x c - M) and
-// S = sum 2^(x c - M) (x c - M), and moves them when m grows: Z' = Z 2^(M - M'), S' = 2^(M - M') (S + (M - M') Z).
-// M is one fp32 number that every later step uses, so its rounding is in no result.  entropy = ln 2 (log2 Z - S / Z): S <= 0, so
-// nothing cancels.
+// With z_j = scale * x_j:  lse = ln sum_j exp z_j,  logprob_t = z_t - lse,  entropy = lse - sum_j p_j z_j.
+// One pass over the row: every thread keeps a reference M, Z = sum exp(scale (x - M)) and S = sum exp(scale (x - M)) (x - M).  M
+// starts as the largest logit of the warp's first loads and follows only what is above it by more than 2^6 in weight (Z' = Z f,
+// S' = f (S + d Z), f = exp(scale d), d = M - M'): a reference that followed every new largest logit would move in some
+// lane of a warp at nearly every step.  entropy = ln Z - scale S / Z, and with M within 2^6 of the row's largest no digits cancel
+// but those that a factor of 64 is worth (ln 64 = 4.2 beside an entropy of up to ln V).
+// An element costs a conversion, half a maximum and half a clamp (in pairs, in its own type), a 2^x and three fp32 operations:
+// the exponent is x c - fl(M c), c = scale log2(e), and what the rounding of M c put in is taken out of the sums at the end.
 //
-// Top alternatives, in the order of (logit descending, id ascending): a thread knows its best element.  The threads are cut
-// into G >= k groups; the smallest of the groups' best elements has at least k elements at or above it, so only elements from it
-// on can be among the k, and only threads whose best element is have any.  Those threads' elements are read again (from the
-// L2, a few per cent of the row), what passes is collected, and an element's place is the number of elements before it.
-// Where the row is laid out so that too many pass, the k best are found one after the other.
+// Top alternatives, in the order of (logit descending, id ascending): a thread knows its largest logit.  A value `from` is
+// found, by halving intervals, that at least k threads and few more reach with theirs: the k best are at or above it, and only
+// these threads hold any such.  Their elements are read again (from the L2, a few per cent of the row), what passes is
+// collected, and an element's place is the number of elements before it.  Where more pass than fit, the k best are found one
+// after the other.
 //
 // Few long rows are shared by the CTAs of a cluster, which send their sums and their k best to the first one.
 // Bound by memory for many rows, by the length of this chain for a few.
@@ -23,12 +25,11 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kResident = 5;        // blocks of an SM (51 registers a thread; with 4 many rows took 4 % longer, 320 rows 20 %)
 constexpr int kMaxK = 64;
-// Elements collected at most.  What a row of equal logits passes, or all there are if some thread has none, fits: 8 x 256
-// and up to 14 single elements at the ends.
-constexpr int kCand = 2112;
+constexpr int kCand = 1024;         // elements collected at most
 constexpr int kMaxParts = 8;        // CTAs of a row (the portable cluster size)
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct ScoreArgs {
   const void *x;
@@ -40,20 +41,14 @@ struct ScoreArgs {
   int V, n_ids, k;
 };
 
-template <typename T, int N> struct alignas(16) Vec {
-  T v[N];
-};
-
 // Order of elements as one unsigned number: logits descending, then ids ascending; 0 is before no element.  -0 and 0 are equal.
-__device__ __forceinline__ uint64_t key_of(float x, uint32_t id) {
-  uint32_t b = __float_as_uint(x + 0.f);
-  b = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return uint64_t(b) << 32 | uint32_t(~id);
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float key_value(uint64_t key) {
-  const uint32_t b = uint32_t(key >> 32);
-  return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
-}
+__device__ __forceinline__ float value_of(uint32_t b) { return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b); }
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t id) { return uint64_t(ordered(x)) << 32 | uint32_t(~id); }
+__device__ __forceinline__ float key_value(uint64_t key) { return value_of(uint32_t(key >> 32)); }
 __device__ __forceinline__ uint32_t key_id(uint64_t key) { return ~uint32_t(key); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -68,24 +63,81 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int o) { return __shfl_xor_sync(0xffffffffu, (unsigned long long)v, o); }
 
-// Sums of a set of elements: largest logit, Z and S relative to M = fl(m c).  m is NaN if any element is.
-struct Sums {
-  float m, z, s;
+// What masked elements count as: far below any logit that matters, and times log2(e) still finite.
+__device__ __forceinline__ float lowest(__half) { return -65504.f; }
+__device__ __forceinline__ float lowest(__nv_bfloat16) { return -0x1p120f; }
+__device__ __forceinline__ float lowest(float) { return -0x1p120f; }
+
+// Sixteen bytes of a row: its elements in fp32 and their largest (NaN if one is).  CLAMP: elements below lowest(T) come as
+// lowest(T): 0 times -inf would be NaN where a weight of 0 is meant.
+template <bool CLAMP = false> __device__ __forceinline__ float open(const uint4 &r, float (&e)[8], __half) {
+  uint32_t w[4] = {r.x, r.y, r.z, r.w}, t0, t1;
+  asm("max.NaN.f16x2 %0, %1, %2;\n" : "=r"(t0) : "r"(w[0]), "r"(w[1]));
+  asm("max.NaN.f16x2 %0, %1, %2;\n" : "=r"(t1) : "r"(w[2]), "r"(w[3]));
+  asm("max.NaN.f16x2 %0, %1, %2;\n" : "=r"(t0) : "r"(t0), "r"(t1));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (CLAMP) asm("max.NaN.f16x2 %0, %0, %1;\n" : "+r"(w[i]) : "r"(0xfbfffbffu));
+    const float2 v = __half22float2(u32_as_h2(w[i]));
+    e[2 * i] = v.x;
+    e[2 * i + 1] = v.y;
+  }
+  const float2 t = __half22float2(u32_as_h2(t0));
+  return max_nan(t.x, t.y);
+}
+template <bool CLAMP = false> __device__ __forceinline__ float open(const uint4 &r, float (&e)[8], __nv_bfloat16) {
+  uint32_t w[4] = {r.x, r.y, r.z, r.w}, t0, t1;
+  asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(t0) : "r"(w[0]), "r"(w[1]));
+  asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(t1) : "r"(w[2]), "r"(w[3]));
+  asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(t0) : "r"(t0), "r"(t1));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (CLAMP) asm("max.NaN.bf16x2 %0, %0, %1;\n" : "+r"(w[i]) : "r"(0xfb80fb80u));
+    e[2 * i] = __uint_as_float(w[i] << 16);
+    e[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  return max_nan(__uint_as_float(t0 << 16), __uint_as_float(t0 & 0xffff0000u));
+}
+template <bool CLAMP = false> __device__ __forceinline__ float open(const uint4 &r, float (&e)[4], float) {
+  e[0] = __uint_as_float(r.x);
+  e[1] = __uint_as_float(r.y);
+  e[2] = __uint_as_float(r.z);
+  e[3] = __uint_as_float(r.w);
+  const float top = max_nan(max_nan(e[0], e[1]), max_nan(e[2], e[3]));
+  if (CLAMP) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e[j] = fmaxf(e[j], -0x1p120f);
+  }
+  return top;
+}
+
+// Sums of a set of elements: largest logit m (NaN if any element is), reference M, Z and S.
+struct alignas(16) Sums {
+  float m, M, z, s;
 };
-// The reference of a largest logit; an empty side's is 0, so that x c - M stays -inf.
-__device__ __forceinline__ float reference(float m, float c) { return m == -INFINITY ? 0.f : __fmul_rn(m, c); }
-// b into a.
-__device__ __forceinline__ void join(Sums &a, const Sums &b, float c) {
-  const float m = max_nan(a.m, b.m), M = reference(m, c);
-  auto moved = [&](const Sums &o, float &z, float &s) {
-    const float d = __fsub_rn(reference(o.m, c), M), f = ex2(d);
-    z = o.z == 0.f ? 0.f : o.z * f;
-    s = o.z == 0.f ? 0.f : f * fmaf(d, o.z, o.s);
-  };
-  float za, sa, zb, sb;
-  moved(a, za, sa);
-  moved(b, zb, sb);
-  a = {m, za + zb, sa + sb};
+// z and s moved to reference M.  Nothing is left where the factor is 0 (0 times an infinite difference would be NaN) or where
+// nothing was (z = 0, whose reference does not count).
+__device__ __forceinline__ void move_to(float M, float c, const Sums &o, float &z, float &s) {
+  const float d = o.M - M, f = ex2(__fmul_rn(d, c));
+  const bool any = f != 0.f && o.z != 0.f;
+  z = any ? o.z * f : 0.f;
+  s = any ? f * fmaf(d, o.z, o.s) : 0.f;
+}
+// The sums of n parts, in their order.
+template <typename At> __device__ __forceinline__ Sums join(int n, float c, At at) {
+  Sums u = {-INFINITY, -INFINITY, 0.f, 0.f};
+  for (int i = 0; i < n; ++i) {
+    const Sums o = at(i);
+    u.m = max_nan(u.m, o.m);
+    if (o.z != 0.f) u.M = fmaxf(u.M, o.M);
+  }
+  for (int i = 0; i < n; ++i) {
+    float z, s;
+    move_to(u.M, c, at(i), z, s);
+    u.z += z;
+    u.s += s;
+  }
+  return u;
 }
 
 // What a CTA of a cluster sends to the first one.
@@ -95,16 +147,17 @@ struct Part {
 };
 
 template <typename T, int PARTS>
-__global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreArgs p) {
+__global__ void __launch_bounds__(kThreads, kResident) score_kernel(const ScoreArgs p) {
   pdl_enter();
   constexpr int VE = 16 / int(sizeof(T));
-  using V4 = Vec<T, VE>;
   __shared__ Part parts[PARTS];
   __shared__ uint64_t cand[kCand];
-  __shared__ uint64_t s_key[kWarps];
+  __shared__ uint32_t s_key[kThreads];
+  __shared__ uint64_t s_best[kWarps];
   __shared__ Sums s_sums[kWarps];
   __shared__ uint8_t s_lane[kWarps][32];
   __shared__ int s_n;
+  __shared__ uint32_t s_from;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int part = PARTS > 1 ? int(cluster_rank()) : 0;
   const int64_t row = blockIdx.x / PARTS;
@@ -115,109 +168,199 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreArgs p) {
   const int head = min(p.V, int((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / int(sizeof(T)));
   const int nv = (p.V - head) / VE, tail = p.V - head - nv * VE;
   const int per = (nv + PARTS - 1) / PARTS, v0 = min(nv, part * per), v1 = min(nv, v0 + per);
-  const V4 *vec = reinterpret_cast<const V4 *>(x + head);
+  const uint4 *vec = reinterpret_cast<const uint4 *>(x + head);
   const bool has_head = part == 0 && tid < head, has_tail = part == 0 && tid < tail;
   const int tail_id = head + nv * VE + tid;
 
-  Sums u = {-INFINITY, 0.f, 0.f};
-  float M = 0.f;
-  // the thread's best element; its first one where all are -inf
-  int best = has_head ? tid : (v0 + tid < v1 ? head + (v0 + tid) * VE : (has_tail ? tail_id : -1));
-  auto take = [&](auto n, const float *e, int id) {
-    constexpr int N = decltype(n)::value;
-    float top = e[0];
-#pragma unroll
-    for (int j = 1; j < N; ++j) top = max_nan(top, e[j]);
-    if (!(top <= u.m)) {
-      const float m = max_nan(u.m, top), Mn = reference(m, c), d = __fsub_rn(M, Mn);
-      if (u.z != 0.f) {
-        const float f = ex2(d);
-        u.s = f * fmaf(d, u.z, u.s);
-        u.z *= f;
-      }
-      u.m = m;
-      M = Mn;
-#pragma unroll
-      for (int j = N - 1; j >= 0; --j)
-        if (e[j] == top) best = id + j;
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      // 0 times -inf would be NaN: an exponent this low is 0 as well
-      const float t = fmaxf(fmaf(e[j], c, -M), -1e4f), w = ex2(t);
-      u.z += w;
-      u.s = fmaf(w, t, u.s);
-    }
+  const bool any = has_head || has_tail || v0 + tid < v1;
+  float m = -INFINITY, M = 0.f, Mc = 0.f, limit = -INFINITY;   // Mc = fl(M c)
+  const float slack = 6.f / c;
+  float z = 0.f, zs = 0.f;   // sums of 2^t and 2^t t, t = x c - Mc
+  auto follow = [&](float top) {
+    const float to = __fmul_rn(top, c), d = Mc - to, f = ex2(d);
+    const bool none = limit == -INFINITY || f == 0.f;   // no element yet, or 0 times an infinite d
+    zs = none ? 0.f : f * fmaf(d, z, zs);
+    z = none ? 0.f : f * z;
+    M = top;
+    Mc = to;
+    limit = top + slack;
+  };
+  auto add = [&](float e) {
+    const float t = fmaf(e, c, -Mc), w = ex2(t);
+    z += w;
+    zs = fmaf(w, t, zs);
   };
   auto one = [&](int id) {
     const float e = to_f32(x[id]);
-    take(std::integral_constant<int, 1>{}, &e, id);
+    m = max_nan(m, e);
+    if (!(e <= limit)) follow(e);
+    add(fmaxf(e, lowest(T())));
   };
-  if (has_head) one(tid);
-  constexpr int kBatch = 4;   // loads in flight
-  for (int v = v0 + tid; v < v1; v += kBatch * kThreads) {
-    V4 r[kBatch];
+  // the first given token's logit on its way
+  const int64_t asked = row * p.n_ids + tid;
+  const int id = tid < p.n_ids && part == 0 ? p.ids[asked] : -1;
+  const float logit = id >= 0 && id < p.V ? to_f32(x[id]) : 0.f;
+  constexpr int kBatch = 4, kStep = kBatch * kThreads;   // loads in flight
+  auto batch = [&](int from, auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    const int v = from + tid;
+    uint4 r[kBatch];
+    float e[kBatch][VE], top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (v + i * kThreads < v1) r[i] = vec[v + i * kThreads];
+      if (kWhole || v + i * kThreads < v1) r[i] = vec[v + i * kThreads];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (v + i * kThreads < v1) {
-        float e[VE];
+      if (kWhole || v + i * kThreads < v1) top = max_nan(top, open<true>(r[i], e[i], T()));
+    m = max_nan(m, top);
+    if (from == v0) {   // the first reference: the largest of the warp's first loads
+      const float high = value_of(__reduce_max_sync(0xffffffffu, ordered(top)));
+      if (fabsf(high) < INFINITY) follow(high);
+    }
+    if (!(top <= limit)) follow(top);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) e[j] = to_f32(r[i].v[j]);
-        take(std::integral_constant<int, VE>{}, e, head + (v + i * kThreads) * VE);
+    for (int i = 0; i < kBatch; ++i)
+      if (kWhole || v + i * kThreads < v1) {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) add(e[i][j]);
       }
-  }
+  };
+  int from = v0;
+  for (; from + kStep <= v1; from += kStep) batch(from, std::true_type{});
+  if (from < v1) batch(from, std::false_type{});
+  if (has_head) one(tid);
   if (has_tail) one(tail_id);
-
+  // t was short of (x - M) c by Mc - M c, the product's rounding; then zs in units of x
+  const float off = fmaf(M, c, -Mc), g = ex2(-off);
+  z *= g;
+  zs = fmaf(zs, g, -off * z) / c;
+  if (m == -INFINITY) z = zs = 0.f;
+  if (fabsf(m) < INFINITY && !((lowest(T()) - M) * c < -200.f && fabsf(M) < 0x1p100f && c > 0x1p-40f && c < 64.f)) {
+    // Masked elements may have had weight, or products been infinite (largest logits near the type's lowest or above 2^100,
+    // extreme scales): again, with differences that are clamped.
+    z = zs = 0.f;
+    M = m;
+    auto again = [&](float e) {
+      const float d = fmaxf(e - M, -3.402823466e38f), w = ex2(__fmul_rn(d, c));
+      z += w;
+      zs = fmaf(w, d, zs);
+    };
+    for (int v = v0 + tid; v < v1; v += kThreads) {
+      float e[VE];
+      open(vec[v], e, T());
+      for (int j = 0; j < VE; ++j) again(e[j]);
+    }
+    if (has_head) again(to_f32(x[tid]));
+    if (has_tail) again(to_f32(x[tail_id]));
+  }
   // ---- the CTA's sums
-  const float own_m = u.m;
+  const uint32_t key = any ? ordered(m) : 0;   // 0: below every logit
+  Sums u;
+  {
+    const uint32_t high = __reduce_max_sync(0xffffffffu, z != 0.f ? ordered(M) : 0u);
+    u.M = high ? value_of(high) : 0.f;
+    move_to(u.M, c, Sums{m, M, z, zs}, u.z, u.s);
+    const float most = value_of(__reduce_max_sync(0xffffffffu, ordered(m)));
+    u.m = __any_sync(0xffffffffu, m != m) ? __int_as_float(0x7fc00000) : most;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums b = {__shfl_xor_sync(0xffffffffu, u.m, o), __shfl_xor_sync(0xffffffffu, u.z, o), __shfl_xor_sync(0xffffffffu, u.s, o)};
-    join(u, b, c);
+    for (int o = 16; o > 0; o >>= 1) {
+      u.z += __shfl_xor_sync(0xffffffffu, u.z, o);
+      u.s += __shfl_xor_sync(0xffffffffu, u.s, o);
+    }
   }
   if (lane == 0) s_sums[warp] = u;
-  const uint64_t key = p.k > 0 && best >= 0 ? key_of(own_m, uint32_t(best)) : 0;
-  uint64_t from = key;
-  // groups of 32, 16, 8 or 4 threads: their best elements, the smallest of them
-  const int wide = p.k <= 8 ? 32 : (p.k <= 16 ? 16 : (p.k <= 32 ? 8 : 4));
-  for (int o = 1; o < wide; o <<= 1) from = max(from, shfl_xor64(from, o));
-  for (int o = wide; o < 32; o <<= 1) from = min(from, shfl_xor64(from, o));
-  if (lane == 0) s_key[warp] = from;
+  if (p.k > 0) s_key[tid] = key;
   if (tid == 0) s_n = 0;
   if (tid < p.k) parts[part].best[tid] = 0;
   __syncthreads();
-  u = s_sums[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) join(u, s_sums[w], c);
+  u = join(kWarps, c, [&](int w) { return s_sums[w]; });
 
   // ---- the CTA's k best (a row that holds a NaN has none)
   if (p.k > 0 && u.m == u.m) {
+    // the largest value (as an ordered number) that at least k threads reach, or one near it
+    if (warp == 0) {
+      uint32_t mine[kWarps], low = ~0u, high = ordered(u.m);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) from = min(from, s_key[w]);
-    auto offer = [&](float e, int id) {
-      const uint64_t mine = key_of(e, uint32_t(id));
-      if (mine >= from) {
-        const int at = atomicAdd(&s_n, 1);
-        if (at < kCand) cand[at] = mine;
+      for (int w = 0; w < kWarps; ++w) {
+        mine[w] = s_key[w * 32 + lane];
+        low = min(low, mine[w]);
       }
+      low = __reduce_min_sync(0xffffffffu, low);   // every thread reaches it
+      while (low < high) {
+        const uint32_t mid = low + (high - low + 1) / 2;
+        int n = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) n += mine[w] >= mid;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (n >= p.k) {
+          low = mid;
+          if (n <= p.k + p.k / 4) break;
+        } else {
+          high = mid - 1;
+        }
+      }
+      if (lane == 0) s_from = low;
+    }
+    __syncthreads();
+    const uint32_t from = s_from;
+    const float least = value_of(from);   // -0 counts as 0; from = 0 is NaN, below which nothing is
+    auto offer = [&](float e, int id) {
+      const int place = atomicAdd(&s_n, 1);
+      if (place < kCand) cand[place] = key_of(e, uint32_t(id));
     };
     const unsigned who = __ballot_sync(0xffffffffu, key != 0 && key >= from);
     if (who >> lane & 1) s_lane[warp][__popc(who & ((1u << lane) - 1))] = uint8_t(lane);
     __syncwarp();
-    if (has_head) offer(to_f32(x[tid]), tid);
-    if (has_tail) offer(to_f32(x[tail_id]), tail_id);
     const int each = (v1 - v0 + kThreads - 1) / kThreads, total = __popc(who) * each;
-    for (int i = lane; i < total; i += 32) {
-      const int n = i / each, v = v0 + warp * 32 + s_lane[warp][n] + (i - n * each) * kThreads;
-      if (v >= v1) continue;
-      const V4 r = vec[v];
+    // the elements of these threads that `pass`
+    auto collect = [&](auto pass) {
+      if (has_head && pass(to_f32(x[tid]))) offer(to_f32(x[tid]), tid);
+      if (has_tail && pass(to_f32(x[tail_id]))) offer(to_f32(x[tail_id]), tail_id);
+      for (int i = lane; i < total; i += 32) {
+        const int n = i / each, v = v0 + warp * 32 + s_lane[warp][n] + (i - n * each) * kThreads;
+        if (v >= v1) continue;
+        float e[VE];
+        if (!pass(open(vec[v], e, T()))) continue;
 #pragma unroll
-      for (int j = 0; j < VE; ++j) offer(to_f32(r.v[j]), head + v * VE + j);
-    }
+        for (int j = 0; j < VE; ++j)
+          if (pass(e[j])) offer(e[j], head + v * VE + j);
+      }
+    };
+    collect([&](float e) { return !(e < least); });
     __syncthreads();
+    if (s_n > kCand) {
+      // Many equal to `least` (masked rows with fewer than k others, rows of few values): those above it, then of the equal
+      // ones the first that are needed, in the order of their ids.
+      __syncthreads();
+      if (tid == 0) s_n = 0;
+      __syncthreads();
+      collect([&](float e) { return e > least; });
+      __syncthreads();
+      int found = s_n;
+      __syncthreads();
+      if (found > kCand - 32 * VE - 2 * VE) {
+        if (tid == 0) s_n = kCand + 1;
+      } else if (warp == 0) {
+        auto count = [&] {   // after the lanes' offers
+          __syncwarp();
+          found = *reinterpret_cast<volatile int *>(&s_n);
+          __syncwarp();
+        };
+        if (has_head && to_f32(x[tid]) == least) offer(least, tid);
+        count();
+        for (int v = v0; v < v1 && found < p.k; v += 32) {
+          float e[VE];
+          if (v + lane < v1 && open(vec[v + lane], e, T()) >= least) {
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+              if (e[j] == least) offer(e[j], head + (v + lane) * VE + j);
+          }
+          count();
+        }
+        if (found < p.k && has_tail && to_f32(x[tail_id]) == least) offer(least, tail_id);
+      }
+      __syncthreads();
+    }
     const int n = s_n;
     if (n <= kCand) {
       for (int i = tid; i < n; i += kThreads) {
@@ -238,17 +381,18 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreArgs p) {
         if (has_head) look(to_f32(x[tid]), tid);
         if (has_tail) look(to_f32(x[tail_id]), tail_id);
         for (int v = v0 + tid; v < v1; v += kThreads) {
-          const V4 r = vec[v];
+          float e[VE];
+          open(vec[v], e, T());
 #pragma unroll
-          for (int j = 0; j < VE; ++j) look(to_f32(r.v[j]), head + v * VE + j);
+          for (int j = 0; j < VE; ++j) look(e[j], head + v * VE + j);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mine = max(mine, shfl_xor64(mine, o));
         __syncthreads();
-        if (lane == 0) s_key[warp] = mine;
+        if (lane == 0) s_best[warp] = mine;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mine = max(mine, s_key[w]);
+        for (int w = 0; w < kWarps; ++w) mine = max(mine, s_best[w]);
         last = mine;
         if (tid == 0) parts[part].best[found] = mine;
       }
@@ -267,35 +411,37 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreArgs p) {
       if (tid == 0) {
         const uint32_t to = map_to_rank(&parts[part].sums, 0);
         asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to), "f"(u.m) : "memory");
-        asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to + 4), "f"(u.z) : "memory");
-        asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to + 8), "f"(u.s) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to + 4), "f"(u.M) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to + 8), "f"(u.z) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to + 12), "f"(u.s) : "memory");
       }
     }
     __syncwarp();
     cluster_sync();
     if (part != 0) return;
-#pragma unroll
-    for (int w = 1; w < PARTS; ++w) join(u, parts[w].sums, c);
+    if (tid == 0) parts[0].sums = u;
+    __syncthreads();
+    u = join(PARTS, c, [&](int w) { return parts[w].sums; });
   } else {
     __syncthreads();
   }
 
-  const float Mr = reference(u.m, c), nan = __int_as_float(0x7fc00000);
-  const float lz = log2f(u.z);
+  const float nan = __int_as_float(0x7fc00000), lz = logf(u.z);
   auto logprob = [&](float e) {
     if (u.m != u.m) return nan;
     if (u.m == -INFINITY) return -INFINITY;
     if (u.m == INFINITY) return e == INFINITY ? nan : -INFINITY;
-    return (fmaf(e, c, -Mr) - lz) * kLn2;
+    return fmaf(e - u.M, p.scale, -lz);
   };
-  for (int i = tid; i < p.n_ids; i += kThreads) {
-    const int id = p.ids[row * p.n_ids + i];
-    p.logprob[row * p.n_ids + i] = id >= 0 && id < p.V ? logprob(to_f32(x[id])) : nan;
+  if (tid < p.n_ids) p.logprob[asked] = id >= 0 && id < p.V ? logprob(logit) : nan;
+  for (int i = tid + kThreads; i < p.n_ids; i += kThreads) {
+    const int j = p.ids[row * p.n_ids + i];
+    p.logprob[row * p.n_ids + i] = j >= 0 && j < p.V ? logprob(to_f32(x[j])) : nan;
   }
   if (tid == 0) {
     const bool finite = fabsf(u.m) < INFINITY;
-    if (p.lse) p.lse[row] = finite ? (Mr + lz) * kLn2 : u.m;
-    if (p.entropy) p.entropy[row] = finite ? (lz - u.s / u.z) * kLn2 : (u.m == -INFINITY ? 0.f : nan);
+    if (p.lse) p.lse[row] = finite ? fmaf(u.M, p.scale, lz) : u.m;
+    if (p.entropy) p.entropy[row] = finite ? fmaf(-p.scale, u.s / u.z, lz) : (u.m == -INFINITY ? 0.f : nan);
   }
   const int there = u.m == u.m ? min(p.k, p.V) : 0;
   for (int i = tid; i < PARTS * p.k; i += kThreads) {
@@ -335,10 +481,12 @@ template <typename T, int PARTS> int launch_parts(const ScoreArgs &p, int64_t T_
 }
 
 template <typename T> int launch_score(const ScoreArgs &p, int64_t T_, cudaStream_t st) {
-  // a row's CTAs: as many as leave every SM its 4 blocks and a CTA at least 2048 elements
-  const int64_t slots = int64_t(num_sms()) * 4;
+  // A row's CTAs: as many as still run all at once, with at least 4096 elements each.  Rows of 131072 in bf16, 1, 2, 4 and 8 CTAs:
+  // 1 row 12.7, 9.3, 7.5, 6.9 us; 64 rows 14.4, 11.3, 11.4, 11.9; 150 rows 20.9, 18.4, 16.0, 21.2; 320 rows 29.0, 23.5, 28.2,
+  // 37.1; 600 rows 36.2, 40.9, 47.8, 62.8; one row of 32000 in fp32 7.2, 6.5, 5.8, 6.2.
+  const int64_t slots = int64_t(num_sms()) * kResident;
   int n = 1;
-  while (n < kMaxParts && T_ * n < slots && p.V / (2 * n) >= 2048) n *= 2;
+  while (n < kMaxParts && T_ * 2 * n <= slots && p.V / (2 * n) >= 4096) n *= 2;
   if (n == 1) return launch_parts<T, 1>(p, T_, st);
   if (n == 2) return launch_parts<T, 2>(p, T_, st);
   if (n == 4) return launch_parts<T, 4>(p, T_, st);
