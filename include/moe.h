@@ -580,7 +580,7 @@ int moe_quantize_rows(const void *x, int64_t x_stride, int dtype, int64_t T, int
  * other rows or on which kernel runs: a token's outputs are the same bits alone and in any batch.
  * workspace: >= moe_linear_w8a8_workspace_size(M, N, K) bytes; one sized for M serves every call of fewer rows with the same N
  * and K.  Its contents have no influence.  Rows of w that do not all start on 16 bytes (K % 16 != 0 among them) are copied into it
- * on every call. */
+ * on every call; where they do, the size for N = 0 is enough (none up to 16 rows). */
 size_t moe_linear_w8a8_workspace_size(int64_t M, int64_t N, int64_t K);
 int moe_linear_w8a8(const int8_t *a, int64_t a_stride, const float *a_scale, const int8_t *w, int64_t w_stride,
                     const float *w_scale, const float *bias, int64_t M, int64_t N, int64_t K, void *out,

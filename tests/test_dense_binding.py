@@ -171,4 +171,4 @@ def test_linear_workspace_size(built):
     assert size(4, 8, 0) == 0 and size(-1, 8, 8) == 0 and size(4, 8, 131072) == 0
     for N, K in ((5, 15), (4096, 4096), (33, 1408), (6144, 131071)):
         got = [size(M, N, K) for M in (0, 1, 8, 16, 17, 32, 33, 64, 200, 1000, 8192, 100000)]
-        assert got[0] >= N * K and all(b >= a for a, b in zip(got, got[1:]))      # serves every call of fewer rows
+        assert got[0] >= N * K and got[0] == got[3] and size(16, 0, K) == 0 and size(17, 0, K) >= 34 * K and all(b >= a for a, b in zip(got, got[1:]))      # serves every call of fewer rows

@@ -4,6 +4,7 @@
 // The sum is exact in 32-bit integers, so its order and its split over warps and CTAs do not show: every form below gives the
 // same bits.
 #include <algorithm>
+#include <atomic>
 
 #include "linear8.cuh"
 #include "tc_ptx.cuh"
@@ -24,19 +25,15 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const int8_t *w, int64_t 
 
 // ---- a few rows: the weights as a stream ------------------------------------------------------------------------------
 //
-// A CTA takes 16 channels and 8 MT rows over a range of K; its 8 warps take the range's 256-wide pieces in turn and add their
+// A CTA takes 16 CT channels and 8 MT rows over a range of K; its 8 warps take the range's pieces in turn and add their
 // sums up in shared memory, the CTAs of a cluster (splits of K) theirs in the first one's.  The weights are the A operand
-// of m16n8k32 (s8, s32 accumulators) straight from 16-byte loads: the order of a sum's terms is free, so a lane's
-// four consecutive words stand for the four 4-wide slots that two MMAs want of it, and the rows' values, read from
-// shared memory the same way, match.
-constexpr int kStreamThreads = 256, kStreamWarps = 8, kChunk = 256;
+// of m16n8k16 (f16, fp32 accumulators), converted in registers from 16-byte loads: the order of a sum's terms is free, so a
+// lane's 16 consecutive values stand for the slots that four MMAs want of it, and the rows' values, f16 in shared memory and
+// read the same way, match.  (m16n8k32 on the integers themselves takes 128 cycles a sub-core on this chip: one row of 4096 x 6144
+// 8.2 us, 16 rows 16.3 us.)  A warp's accumulators are emptied into the 32-bit integers after 1024 of K: up to there an
+// fp32 sum of these products is exact.
+constexpr int kStreamThreads = 256, kStreamWarps = 8, kStreamSmem = 72 * 1024;
 
-__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint4 load_stream(const int8_t *p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];\n"
@@ -45,124 +42,186 @@ __device__ __forceinline__ uint4 load_stream(const int8_t *p) {
   return v;
 }
 
-// phase: K range whose rows' values fit the shared memory; split: K range of a CTA (both multiples of kChunk)
-template <int MT>
-__global__ void __launch_bounds__(kStreamThreads) linear8_stream_kernel(const LinearArgs p, int splits, int split, int phase,
-                                                                        int vector_rows) {
+// phase: K range whose rows' values fit the shared memory; split: K range of a CTA (both multiples of 256)
+template <int MT, int CT>
+__global__ void __launch_bounds__(kStreamThreads, 2) linear8_stream_kernel(const LinearArgs p, int splits, int split, int phase,
+                                                                           int vector_rows) {
   pdl_enter();
-  extern __shared__ __align__(16) int8_t s_rows[];   // 8 MT rows of phase + 64 bytes: two rows' pieces share no bank
-  __shared__ int s_sum[8 * MT][16];
+  constexpr int kChunk = 256 / CT, kPieces = kChunk / 64;   // K of a step: 8 loads a lane
+  extern __shared__ __align__(16) uint8_t s_rows[];         // 8 MT rows of phase f16 values + 16 bytes: no bank conflicts
+  __shared__ int s_sum[8 * MT][16 * CT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int rank = splits > 1 ? int(cluster_rank()) : 0;
-  const int n0 = int(blockIdx.x) / splits * 16;
-  const int64_t m0 = int64_t(blockIdx.y) * (8 * MT);
-  const int rows = int(min(int64_t(8 * MT), p.M - m0));
+  const int n0 = int(blockIdx.x) / splits * (16 * CT);
+  const int rows = int(p.M);
   const int kr = (p.K + 15) & ~15, k0 = rank * split, k1 = min(kr, k0 + split);
-  const int pitch = phase + 64;
-  for (int i = tid; i < 8 * MT * 16; i += kStreamThreads) (&s_sum[0][0])[i] = 0;
+  const int pitch = 2 * phase + 16;
+  for (int i = tid; i < 8 * MT * 16 * CT; i += kStreamThreads) (&s_sum[0][0])[i] = 0;
   if (splits > 1) {   // every CTA's sums are zero: waited for before the first one's are added to
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
   }
 
-  int c[MT][4];
+  float c[CT][MT][4];
+  auto clear = [&] {
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+    for (int u = 0; u < CT; ++u)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[t][i] = 0;
-  const bool lo_there = n0 + g < p.N, hi_there = n0 + g + 8 < p.N;
-  const int8_t *w_lo = p.w + int64_t(n0 + g) * p.w_stride, *w_hi = w_lo + 8 * p.w_stride;
-  uint4 lo[4], hi[4];
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[u][t][i] = 0.f;
+  };
+  auto flush = [&] {
+#pragma unroll
+    for (int u = 0; u < CT; ++u)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (8 * t + 2 * q + (i & 1) < rows)
+            atomicAdd(&s_sum[8 * t + 2 * q + (i & 1)][16 * u + g + 8 * (i >> 1)], __float2int_rn(c[u][t][i]));
+  };
+  clear();
+  const int8_t *w = p.w + int64_t(n0 + g) * p.w_stride + 16 * q;
+  uint4 r[2 * CT][kPieces];
   auto fetch = [&](int k, int end) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int at = k + 64 * j + 16 * q;
-      lo[j] = lo_there && at < end ? load_stream(w_lo + at) : make_uint4(0, 0, 0, 0);
-      hi[j] = hi_there && at < end ? load_stream(w_hi + at) : make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < 2 * CT; ++i)
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+        r[i][j] = n0 + g + 8 * i < p.N && k + 64 * j + 16 * q < end ? load_stream(w + 8 * i * p.w_stride + k + 64 * j) : make_uint4(0, 0, 0, 0);
   };
   for (int ph = k0; ph < k1; ph += phase) {
     const int end = min(k1, ph + phase);
     int k = ph + warp * kChunk;
     if (k < end) fetch(k, end);
-    __syncthreads();   // the last phase's rows have been read
-    if (vector_rows) {
-      const int per = (end - ph) >> 4;
-      for (int i = tid; i < per * 8 * MT; i += kStreamThreads) {
-        const int r = i / per, at = (i - r * per) << 4;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows) v = *reinterpret_cast<const uint4 *>(p.a + (m0 + r) * p.a_stride + ph + at);
-        *reinterpret_cast<uint4 *>(s_rows + r * pitch + at) = v;
+    __syncthreads();   // the last phase's rows have been read; the sums are zero
+    const int per = (end - ph) >> 4;
+    for (int i = tid; i < per * rows; i += kStreamThreads) {
+      const int m = i / per, at = (i - m * per) << 4;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      const int8_t *src = p.a + m * p.a_stride + ph + at;
+      if (vector_rows) {
+        v = *reinterpret_cast<const uint4 *>(src);
+      } else {
+        int8_t *byte = reinterpret_cast<int8_t *>(&v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (ph + at + j < p.K) byte[j] = src[j];
       }
-    } else {
-      const int per = end - ph;
-      for (int i = tid; i < per * 8 * MT; i += kStreamThreads) {
-        const int r = i / per, at = i - r * per;
-        s_rows[r * pitch + at] = r < rows && ph + at < p.K ? p.a[(m0 + r) * p.a_stride + ph + at] : int8_t(0);
-      }
-    }
-    __syncthreads();
-    while (k < end) {
-      uint4 wl[4], wh[4];
+      uint32_t h[8];
+      const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        wl[j] = lo[j];
-        wh[j] = hi[j];
+        uint32_t two[2];
+        i2f_int8(words[j] ^ 0x80808080u, two, __half());
+        h[2 * j] = two[0];
+        h[2 * j + 1] = two[1];
       }
-      const int8_t *rp = s_rows + g * pitch + (k - ph) + 16 * q;
+      uint4 *dst = reinterpret_cast<uint4 *>(s_rows + m * pitch + 2 * at);
+      dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+    __syncthreads();
+    int steps = 0;
+    while (k < end) {
+      const uint8_t *rp = s_rows + 2 * (k - ph + 16 * q);
+      // the pieces of this step that hold anything: what lies behind has not been written
+      const int here = (end - k + 63) >> 6;
+      uint4 now[2 * CT][kPieces];
+#pragma unroll
+      for (int i = 0; i < 2 * CT; ++i)
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) now[i][j] = r[i][j];
       k += kStreamWarps * kChunk;
       if (k < end) fetch(k, end);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < kPieces; ++j) {
+        if (j >= here) break;
+        uint32_t a[2 * CT][8];
+#pragma unroll
+        for (int i = 0; i < 2 * CT; ++i) {
+          const uint32_t words[4] = {now[i][j].x, now[i][j].y, now[i][j].z, now[i][j].w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint32_t two[2];
+            i2f_int8(words[s] ^ 0x80808080u, two, __half());
+            a[i][2 * s] = two[0];
+            a[i][2 * s + 1] = two[1];
+          }
+        }
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          const uint4 b = *reinterpret_cast<const uint4 *>(rp + t * 8 * pitch + 64 * j);
-          mma_s8(c[t], wl[j].x, wh[j].x, wl[j].y, wh[j].y, b.x, b.y);
-          mma_s8(c[t], wl[j].z, wh[j].z, wl[j].w, wh[j].w, b.z, b.w);
-        }
-    }
-  }
+          // rows past the last one and values past a ragged end: zeros (f16 garbage could be NaN)
+          const bool there = 8 * t + g < rows && 64 * j + 16 * q < 64 * here;
+          const uint8_t *src = rp + (8 * t + g) * pitch + 128 * j;
+          uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
+          if (there && k - kStreamWarps * kChunk + 64 * j + 16 * q < end) {
+            b0 = *reinterpret_cast<const uint4 *>(src);
+            b1 = *reinterpret_cast<const uint4 *>(src + 16);
+          }
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    atomicAdd(&s_sum[8 * t + 2 * q][g], c[t][0]);
-    atomicAdd(&s_sum[8 * t + 2 * q + 1][g], c[t][1]);
-    atomicAdd(&s_sum[8 * t + 2 * q][g + 8], c[t][2]);
-    atomicAdd(&s_sum[8 * t + 2 * q + 1][g + 8], c[t][3]);
+          for (int u = 0; u < CT; ++u) {
+            const uint32_t b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const uint32_t f[4] = {a[2 * u][2 * s], a[2 * u + 1][2 * s], a[2 * u][2 * s + 1], a[2 * u + 1][2 * s + 1]};
+              mma16816(c[u][t], f, b[2 * s], b[2 * s + 1], __half());
+            }
+          }
+        }
+      }
+      if (++steps == 1024 / kChunk) {
+        flush();
+        clear();
+        steps = 0;
+      }
+    }
+    if (steps) {
+      flush();
+      clear();
+    }
   }
   __syncthreads();
   if (splits > 1) {
     asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
     if (rank != 0) {
       const uint32_t to = map_to_rank(&s_sum[0][0], 0);
-      for (int i = tid; i < 16 * rows; i += kStreamThreads)
+      for (int i = tid; i < 16 * CT * rows; i += kStreamThreads)
         asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;\n" ::"r"(to + 4 * i), "r"((&s_sum[0][0])[i]) : "memory");
     }
     __syncwarp();
     cluster_sync();
     if (rank != 0) return;
   }
-  for (int i = tid; i < 16 * rows; i += kStreamThreads) {
-    const int r = i >> 4, n = n0 + (i & 15);
+  for (int i = tid; i < 16 * CT * rows; i += kStreamThreads) {
+    const int m = i / (16 * CT), at = i % (16 * CT), n = n0 + at;
     if (n < p.N)
-      store_out(p.out, p.out_dtype, (m0 + r) * p.out_stride + n, scaled(s_sum[r][i & 15], p.a_scale[m0 + r], p.w_scale[n], p.bias != nullptr, p.bias ? p.bias[n] : 0.f));
+      store_out(p.out, p.out_dtype, m * p.out_stride + n,
+                scaled(s_sum[m][at], p.a_scale[m], p.w_scale[n], p.bias != nullptr, p.bias ? p.bias[n] : 0.f));
   }
 }
 
-template <int MT> int launch_stream(const LinearArgs &p, cudaStream_t st) {
-  const int64_t tiles = cdiv(p.N, 16), chunks = cdiv(p.M, 8 * MT);
+template <int MT, int CT> int launch_stream(const LinearArgs &p, cudaStream_t st) {
+  const int64_t tiles = cdiv(p.N, 16 * CT);
   const int kr = (p.K + 15) & ~15;
-  // splits of K: two CTAs for every SM, at least 512 of K each
+  // splits of K: as many as still run all at once, at least 512 of K each
   int splits = 1;
-  while (splits < 8 && tiles * chunks * splits < 2 * num_sms() && kr / (2 * splits) >= 512) splits *= 2;
-  const int split = int(cdiv(cdiv(kr, splits), kChunk) * kChunk);
-  const int most = 96 * 1024 / (8 * MT) - 64;
-  const int phase = std::min(split, most / kChunk * kChunk);
-  const size_t smem = size_t(8 * MT) * (phase + 64);
+  while (splits < 8 && tiles * splits * 2 <= 2 * num_sms() && kr / (2 * splits) >= 512) splits *= 2;
+  const int split = int(cdiv(cdiv(kr, splits), 256) * 256);
+  const int most = (kStreamSmem / (8 * MT) - 16) / 2 / 256 * 256;
+  const int phase = std::min(split, most);
+  const size_t smem = size_t(8 * MT) * (2 * phase + 16);
   const int vector_rows = p.K % 16 == 0 && p.a_stride % 16 == 0 && aligned16(p.a);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return check_launch("linear_w8a8: cudaGetDevice");
-  if (cudaFuncSetAttribute(linear8_stream_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024) != cudaSuccess)
-    return check_launch("linear_w8a8 attribute");
+  if (dev < 0 || dev >= 64) return set_error(MOE_ERR_UNSUPPORTED, "linear_w8a8: device index %d >= 64", dev);
+  static std::atomic<bool> attr_set[64];
+  if (!attr_set[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(linear8_stream_kernel<MT, CT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem) != cudaSuccess)
+      return check_launch("linear_w8a8 attribute");
+    attr_set[dev].store(true, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -171,20 +230,21 @@ template <int MT> int launch_stream(const LinearArgs &p, cudaStream_t st) {
   attr[1].val.clusterDim.x = unsigned(splits);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(unsigned(tiles * splits), unsigned(chunks));
+  cfg.gridDim = dim3(unsigned(tiles * splits));
   cfg.blockDim = dim3(kStreamThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = splits > 1 ? 2 : 1;
-  cudaLaunchKernelEx(&cfg, linear8_stream_kernel<MT>, p, splits, split, phase, vector_rows);
+  cudaLaunchKernelEx(&cfg, linear8_stream_kernel<MT, CT>, p, splits, split, phase, vector_rows);
   return check_launch("linear_w8a8");
 }
 
-// Rows up to which the weights are streamed past all of them at once.
-constexpr int64_t kStreamRows = 32;
+// Rows up to which the weights are streamed past all of them at once.  24 rows there and on tcgen05: 4096 x 4096 15.7 and 11.6 us,
+// 6144 x 4096 25.0 and 15.3, 2048 x 2048 6.5 and 9.2; 16 rows 8.6, 13.4 and 5.2 there.
+constexpr int64_t kStreamRows = 16;
 
-// The workspace: the weights' rows padded to 16 bytes (used if they need it), then the rows as f16 (many rows).
+// The workspace: the rows as f16 (many rows), then the weights' rows padded to 16 bytes (if they need it).
 size_t padded_bytes(int64_t N, int64_t K) { return align256(size_t(N) * size_t((K + 15) & ~int64_t(15))); }
 bool needs_padding(const int8_t *w, int64_t w_stride, int64_t K) { return K % 16 != 0 || w_stride % 16 != 0 || !aligned16(w); }
 
@@ -218,22 +278,24 @@ extern "C" int moe_linear_w8a8(const int8_t *a, int64_t a_stride, const float *a
   LinearArgs p{a, w, a_scale, w_scale, bias, out, M, a_stride, w_stride, out_stride, int(N), int(K), out_dtype};
   if (N == 1) p.w_stride = (K + 15) & ~int64_t(15);   // a single row's is not looked at
   const bool pad = needs_padding(w, p.w_stride, K), many = M > kStreamRows;
-  const size_t need = (pad || many ? padded_bytes(N, K) : 0) + (many ? linear8_tc_rows_bytes(M, K) : 0);
+  const size_t rows_bytes = many ? linear8_tc_rows_bytes(M, K) : 0, need = rows_bytes + (pad ? padded_bytes(N, K) : 0);
   if (need > 0) {
     if (workspace_bytes < need) return set_error(MOE_ERR_WORKSPACE, "linear_w8a8 workspace %zu < %zu bytes", workspace_bytes, need);
     MOE_REQUIRE(workspace && aligned16(workspace), "workspace must be non-null and 16-byte aligned");
   }
   if (pad) {
     const int pitch = int((K + 15) & ~int64_t(15));
-    int8_t *padded = static_cast<int8_t *>(workspace);
+    int8_t *padded = static_cast<int8_t *>(workspace) + rows_bytes;
     const int64_t blocks = std::min<int64_t>(cdiv(N * pitch, 256), int64_t(num_sms()) * 32);
     launch_pdl(pad_rows_kernel, dim3(unsigned(blocks)), dim3(256), 0, st, w, p.w_stride, N, int(K), pitch, padded);
     MOE_TRY(check_launch("linear_w8a8 padding"));
     p.w = padded;
     p.w_stride = pitch;
   }
-  if (many) return launch_linear8_tc(p, static_cast<char *>(workspace) + padded_bytes(N, K), st);
-  if (M <= 8) return launch_stream<1>(p, st);
-  if (M <= 16) return launch_stream<2>(p, st);
-  return launch_stream<4>(p, st);
+  if (many) return launch_linear8_tc(p, workspace, st);
+  // 16 channels a CTA for few rows and channels, else 32 (the rows' values are read from shared memory half as often): 1 row
+  // 4096 x 4096 5.2 and 5.5 us, 6144 x 4096 7.7 and 7.2, 32768 x 2048 21.1 and 17.6; 16 rows 10.3 and 8.6, 18.1 and 13.4,
+  // 37.6 and 29.2
+  if (M <= 8) return cdiv(N, 16) <= 2 * num_sms() ? launch_stream<1, 1>(p, st) : launch_stream<1, 2>(p, st);
+  return launch_stream<2, 2>(p, st);
 }

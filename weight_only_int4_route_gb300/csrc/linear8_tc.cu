@@ -51,7 +51,10 @@ namespace {
 constexpr int kEpiWarps = 8, kGroups = 2, kGroupWarps = 4;
 constexpr int kConvWarp = kEpiWarps, kRowWarp = kConvWarp + kGroups * kGroupWarps, kWeightWarp = kRowWarp + 1, kMmaWarp = kRowWarp + 2;
 constexpr int kTcThreads = (kRowWarp + 4) * 32;   // whole warpgroups: registers are dealt by them
-constexpr int kEpiRegs = 152, kOtherRegs = 56;
+constexpr int kEpiRegs = 144, kOtherRegs = 64;   // 256 x 144 + 384 x 64 = 640 x 96, all there are
+// CTAs of a cluster at most.  Clusters of 8 with this much shared memory do not all run at once (2048 x 2048, 24 rows: 12 us with 4,
+// 21 with 8), and sizes that are no power of two leave SMs idle (3: 26 us where 2 took 18).
+constexpr int kMaxSplits = 4;
 constexpr int kBM = 128, kBN = 192, kBK = 128, kSegBlocks = 1024 / kBK;
 constexpr int kRowStages = 3, kWStages = 4;
 constexpr int kHalf = kBN * 128, kRowBytes = 2 * kHalf, kWBytes = kBM * kBK;
@@ -59,7 +62,7 @@ constexpr uint32_t kACol0 = 2 * kBN, kACols = kBK / 2;
 static_assert(kWStages % kGroups == 0, "a W stage belongs to one group");
 static_assert(2 * kBN + kGroups * (kBK / 2) <= 512, "tensor memory");
 static_assert(kBN * kBM * 4 <= kRowStages * kRowBytes, "a tile's integers fit the rows' ring");
-constexpr size_t kTcSmem = 1024 + kRowStages * kRowBytes + kWStages * kWBytes + 256;
+constexpr size_t kTcSmem = 1024 + kRowStages * kRowBytes + kWStages * kWBytes + 2 * 16 * kBM * 4 + 256;
 static_assert(kTcSmem <= 232448, "shared memory");
 
 enum : int { kErrFull = 51, kErrFree = 52, kErrReady = 53, kErrD = 54, kErrDrain = 55 };
@@ -69,6 +72,7 @@ struct TcArgs {
   int rows;          // of a tile, a multiple of 16
   int row_tiles, channel_blocks, blocks;   // blocks: 128-wide K blocks
   int splits, per;   // CTAs of a cluster, K blocks of each
+  int vector;        // four results may be stored at once
 };
 
 struct Tile {
@@ -83,16 +87,36 @@ __device__ __forceinline__ Tile tile_at(const TcArgs &t, int i) {
   return {int64_t(group * kG + in % n) * t.rows, in / n * kBM};
 }
 
-template <typename OT>
-__device__ __forceinline__ void store_columns(const LinearArgs &p, int64_t row0, int count, int ch, const int (&acc)[32], int lane) {
-  const bool there = ch < p.N;
-  const float sa = lane < count ? p.a_scale[row0 + lane] : 0.f, sw = there ? p.w_scale[ch] : 0.f;
-  const float b = p.bias && there ? p.bias[ch] : 0.f;
-  OT *o = static_cast<OT *>(p.out) + row0 * p.out_stride + ch;
+// A row's four channels from ch on (those below n) from their integers.
+struct FourScales {
+  float w[4], b[4];
+};
+__device__ __forceinline__ void load_four(const LinearArgs &p, int ch, FourScales &f) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const float v = scaled(acc[j], __shfl_sync(0xffffffffu, sa, j), sw, p.bias != nullptr, b);
-    if (there && j < count) o[j * p.out_stride] = from_f32<OT>(v);
+  for (int j = 0; j < 4; ++j) {
+    f.w[j] = ch + j < p.N ? p.w_scale[ch + j] : 0.f;
+    f.b[j] = p.bias && ch + j < p.N ? p.bias[ch + j] : 0.f;
+  }
+}
+__device__ __forceinline__ void store_four(const LinearArgs &p, bool vector, int64_t row, float sa, int ch, const int4 &acc,
+                                           const FourScales &f) {
+  const bool bias = p.bias != nullptr;
+  const float v[4] = {scaled(acc.x, sa, f.w[0], bias, f.b[0]), scaled(acc.y, sa, f.w[1], bias, f.b[1]),
+                      scaled(acc.z, sa, f.w[2], bias, f.b[2]), scaled(acc.w, sa, f.w[3], bias, f.b[3])};
+  const int64_t at = row * p.out_stride + ch;
+  if (vector && ch + 4 <= p.N) {
+    if (p.out_dtype == MOE_F32) {
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint2 two;
+      if (p.out_dtype == MOE_F16) two = make_uint2(h2_as_u32(__floats2half2_rn(v[0], v[1])), h2_as_u32(__floats2half2_rn(v[2], v[3])));
+      else two = make_uint2(h2_as_u32(__floats2bfloat162_rn(v[0], v[1])), h2_as_u32(__floats2bfloat162_rn(v[2], v[3])));
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = two;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (ch + j < p.N) store_out(p.out, p.out_dtype, at + j, v[j]);
   }
 }
 
@@ -101,7 +125,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   extern __shared__ __align__(1024) uint8_t dsmem[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
   uint8_t *s_row = base, *s_w = s_row + kRowStages * kRowBytes;
-  uint64_t *rfull = reinterpret_cast<uint64_t *>(s_w + kWStages * kWBytes), *done = rfull + kRowStages, *wfull = done + kRowStages,
+  int *s_stage = reinterpret_cast<int *>(s_w + kWStages * kWBytes);   // two halves' 16 rows
+  uint64_t *rfull = reinterpret_cast<uint64_t *>(s_stage + 2 * 16 * kBM), *done = rfull + kRowStages, *wfull = done + kRowStages,
            *wfree = wfull + kWStages, *ready = wfree + kWStages, *d_full = ready + kGroups, *d_empty = d_full + 2, *drain = d_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -153,41 +178,67 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool ok = true;
     for (int i = tile0; ok && i < tiles; i += step) {
       const Tile tile = tile_at(t, i);
-      int acc[3][32];
+      // what the outputs are scaled by, on its way early: four channels a lane, a row a lane of each 32
+      const int ch = tile.ch0 + 4 * lane, count = int(min(int64_t(t.rows), t.p.M - tile.row0));
+      FourScales f;
+      float sa[3];
+      if (t.splits == 1) {
+        load_four(t.p, ch, f);
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          const int row = 32 * (2 * c + half) + lane;
+          sa[c] = row < count ? t.p.a_scale[tile.row0 + row] : 0.f;
+        }
+      }
+      int acc[6][16];
+#pragma unroll
+      for (int c = 0; c < 6; ++c)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[c][j] = 0;
       for (int s = 0; s < segs; ++s, ++seg) {
         if (!(ok = wait_warp(&d_full[seg & 1], seg >> 1, kErrD))) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          const int col = 32 * (2 * c + half);
+        for (int c = 0; c < 6; ++c) {
+          const int col = 32 * (2 * (c >> 1) + half) + 16 * (c & 1);
           if (col >= t.rows) continue;
-          float v[32];
-          tc_ld32(lanes + (seg & 1) * kBN + uint32_t(col), v);
+          uint32_t v[16];
+          tc_ld16(lanes + (seg & 1) * kBN + uint32_t(col), v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) acc[c][j] = s == 0 ? __float2int_rn(v[j]) : acc[c][j] + __float2int_rn(v[j]);
+          for (int j = 0; j < 16; ++j) acc[c][j] += __float2int_rn(__uint_as_float(v[j]));
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&d_empty[seg & 1]);
       }
       if (!ok) break;
+      // 16 rows at a time through shared memory, so that a warp stores whole rows of the tile; with splits all rows stay there
+      // (all of this CTA's MMAs are complete: the rows' ring is free).  Loops, not unrolled code: fetching instructions that are
+      // run once took 7500 cycles for 32 rows.
+#pragma unroll 1
+      for (int c = 0; c < 6; ++c) {
+        const int col = 32 * (2 * (c >> 1) + half) + 16 * (c & 1);
+        if (col >= t.rows) break;   // the same for the half's four warps
+        int *to = (t.splits > 1 ? reinterpret_cast<int *>(s_row) + col * kBM : s_stage + half * (16 * kBM)) + q * 32 + lane;
+        float scale = sa[0];
 #pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        const int col = 32 * (2 * c + half);
-        if (col >= t.rows) continue;
-        if (t.splits > 1) {   // all of this CTA's MMAs are complete: the rows' ring is free
-          int *sums = reinterpret_cast<int *>(s_row);
+        for (int k = 0; k < 6; ++k)
+          if (k == c) {
+            scale = sa[k >> 1];
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (col + j < t.rows) sums[(col + j) * kBM + q * 32 + lane] = acc[c][j];
-        } else {
-          const int64_t row0 = tile.row0 + col;
-          const int count = int(min(int64_t(min(32, t.rows - col)), t.p.M - row0)), ch = tile.ch0 + q * 32 + lane;
-          if (count <= 0) continue;
-          if (t.p.out_dtype == MOE_F32) store_columns<float>(t.p, row0, count, ch, acc[c], lane);
-          else if (t.p.out_dtype == MOE_F16) store_columns<__half>(t.p, row0, count, ch, acc[c], lane);
-          else store_columns<__nv_bfloat16>(t.p, row0, count, ch, acc[c], lane);
+            for (int j = 0; j < 16; ++j) to[j * kBM] = acc[k][j];
+          }
+        if (t.splits > 1) continue;
+        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + half) : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = q + 4 * i;
+          const float row_scale = __shfl_sync(0xffffffffu, scale, 16 * (c & 1) + j);
+          if (col + j < count && ch < t.p.N)
+            store_four(t.p, t.vector, tile.row0 + col + j, row_scale, ch,
+                       *reinterpret_cast<const int4 *>(s_stage + half * (16 * kBM) + j * kBM + 4 * lane), f);
         }
+        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + half) : "memory");
       }
     }
   } else {
@@ -266,19 +317,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_wait(&wfull[n % kWStages], (n / kWStages) & 1, &never, kErrDrain, &g_linear8_error);
     } else if (warp == kMmaWarp && lane == 0) {
       // ------------------------------------------------ MMAs
+      // One thread's path bounds the kernel, so its state is kept in registers: shared-memory addresses, stages and parities
+      // that are stepped, not divided out.
       const uint32_t idesc = idesc_f16(0, kBM, t.rows);
-      uint32_t it = 0, seg = 0;
+      const uint32_t b_rfull = su32(rfull), b_done = su32(done), b_ready = su32(ready), b_dfull = su32(d_full), b_dempty = su32(d_empty);
+      const uint64_t rows0 = sw128_desc(su32(s_row));
+      uint32_t s = 0, s_par = 0, w = 0, w_par = 0, d = 0, d_par = 1;
+      auto wait_at = [&](uint32_t b, uint32_t parity, int code) { return mbar_wait_at(b, parity, abort_flag, code, &g_linear8_error); };
       bool ok = true;
       for (int i = tile0; ok && i < tiles; i += step) {
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const uint32_t first = kb % kSegBlocks, s = it % kRowStages;
-          if (first == 0 && !(ok = wait(&d_empty[seg & 1], (seg >> 1) + 1, kErrD))) break;
-          if (!(ok = wait(&rfull[s], it / kRowStages, kErrFull) && wait(&ready[it % kGroups], it / kGroups, kErrReady))) break;
-          tc_fence_after();
-          tc_mma_kblock_ts<kHalf / 16, false>(tmem + (seg & 1) * kBN, tmem + kACol0 + (it % kGroups) * kACols,
-                                              sw128_desc(su32(s_row + s * kRowBytes)), idesc, first);
-          tc_commit(&done[s]);
-          if (first == kSegBlocks - 1 || kb == nkb - 1) tc_commit(&d_full[seg++ & 1]);
+        for (int left = nkb; ok && left > 0;) {
+          const int n = min(left, kSegBlocks);
+          if (!(ok = wait_at(b_dempty + 8 * d, d_par, kErrD))) break;
+          const uint32_t acc = tmem + d * kBN;
+          for (int kb = 0; kb < n; ++kb) {
+            if (!(ok = wait_at(b_rfull + 8 * s, s_par, kErrFull) && wait_at(b_ready + 8 * w, w_par, kErrReady))) break;
+            tc_fence_after();
+            tc_mma_kblock_ts<kHalf / 16, false>(acc, tmem + kACol0 + w * kACols, rows0 + s * (kRowBytes / 16), idesc, uint32_t(kb));
+            tc_commit_at(b_done + 8 * s);
+            if (++s == kRowStages) s = 0, s_par ^= 1;
+            w_par ^= w;
+            w ^= 1;
+          }
+          if (!ok) break;
+          tc_commit_at(b_dfull + 8 * d);
+          d_par ^= d;
+          d ^= 1;
+          left -= n;
         }
       }
       tc_commit(drain);
@@ -296,23 +361,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   cluster_sync();
   if (*abort_flag == 0 && tile0 < tiles) {
     const Tile tile = tile_at(t, tile0);
-    const int c = threadIdx.x & (kBM - 1), ch = tile.ch0 + c;
-    const int count = int(min(int64_t(t.rows), t.p.M - tile.row0));
-    const uint32_t sums = su32(s_row) + 4 * c;
+    const int ch = tile.ch0 + 4 * lane, count = int(min(int64_t(t.rows), t.p.M - tile.row0));
+    const uint32_t sums = su32(s_row) + 16 * lane;
     if (ch < t.p.N) {
-      const float sw = t.p.w_scale[ch], b = t.p.bias ? t.p.bias[ch] : 0.f;
-#pragma unroll 4
-      for (int row = rank + t.splits * int(threadIdx.x / kBM); row < count; row += t.splits * (kTcThreads / kBM)) {
-        int acc = 0;
-        for (int r = 0; r < t.splits; ++r) {
-          uint32_t from;
-          int v;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(from) : "r"(sums + 4 * kBM * row), "r"(r));
-          asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(v) : "r"(from) : "memory");
-          acc += v;
+      FourScales f;
+      load_four(t.p, ch, f);
+      for (int row = rank + t.splits * warp; row < count; row += t.splits * (kTcThreads / 32)) {
+        const float sa = t.p.a_scale[tile.row0 + row];
+        int4 v[kMaxSplits], acc = make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r) {
+          v[r] = make_int4(0, 0, 0, 0);
+          if (r < t.splits) {
+            uint32_t from;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(from) : "r"(sums + 4 * kBM * row), "r"(r));
+            asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v[r].x), "=r"(v[r].y), "=r"(v[r].z), "=r"(v[r].w) : "r"(from));
+          }
         }
-        store_out(t.p.out, t.p.out_dtype, (tile.row0 + row) * t.p.out_stride + ch,
-                  scaled(acc, t.p.a_scale[tile.row0 + row], sw, t.p.bias != nullptr, b));
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r) acc.x += v[r].x, acc.y += v[r].y, acc.z += v[r].z, acc.w += v[r].w;
+        store_four(t.p, t.vector, tile.row0 + row, sa, ch, acc, f);
       }
     }
   }
@@ -355,20 +423,23 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(const int8_t *__restri
   }
 }
 
-// Rows of a tile and CTAs of a cluster: the pair with the least time by the kernel's own cycle counts (shared memory and MMAs of a
-// K block, 100 between blocks, a tile's start and end, the exchange of a cluster).
+// Rows of a tile and CTAs of a cluster: the pair with the least time by these cycle counts, fitted to measured times: a K block
+// 256 + 4 rows (shared memory) and at least 950 (the MMA thread), a tile's start and end 40 a row, the exchange of a cluster 1300, with
+// four CTAs 16 a row more.  Times of the pairs (row tiles / CTAs), the choice first: 2048 x 2048, 192 rows 2/4 12.2 us, 3/2
+// 12.3, 1/4 13.2, 1/1 19.6; 6144 x 2048, 192 rows 1/2 15.4, 3/1 16.8; 4096 x 4096, 300 rows 2/2 20.6, 4/1 25.4, 2/1 28.4;
+// 4096 x 4096, 1024 rows 8/1 45.2, 6/1 50.0; 6144 x 4096, 1024 rows 6/1 50.4, 8/1 62.4.
 void plan(TcArgs &t, int64_t M, int sms) {
   const int64_t least = cdiv(M, kBN), most = std::max(least, std::min<int64_t>(cdiv(M, 64), least + 6));
   double best = 1e30;
   for (int64_t n = least; n <= most; ++n) {
     const int rows = int(cdiv(cdiv(M, n), 16) * 16);
     const int64_t tiles = cdiv(M, rows) * t.channel_blocks;
-    const double block = std::max(256.0 + 4 * rows, 704.0) + 100;
-    for (int s = 1; s <= 8; ++s) {
+    const double block = std::max(256.0 + 4 * rows, 950.0);
+    for (int s = 1; s <= kMaxSplits; s *= 2) {
       if (s > 1 && tiles * s > sms) break;
       const int per = int(cdiv(t.blocks, s));
       if (cdiv(t.blocks, per) != s) continue;
-      const double time = double(cdiv(tiles * s, sms)) * (per * block + 2000 + 8 * rows) + (s > 1 ? 2500 + 40 * rows / s : 0);
+      const double time = double(cdiv(tiles * s, sms)) * per * block + 40.0 * rows + (s > 1 ? 1300 : 0) + (s > 2 ? 16.0 * rows : 0);
       if (time < best) {
         best = time;
         t.rows = rows;
@@ -395,6 +466,8 @@ int launch_linear8_tc(const LinearArgs &p, void *rows16, cudaStream_t st) {
   t.blocks = int(cdiv(p.K, kBK));
   t.channel_blocks = int(cdiv(p.N, kBM));
   plan(t, p.M, num_sms());
+  const size_t es = dtype_size(p.out_dtype);
+  t.vector = p.out_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & (4 * es - 1)) == 0;
   const int pitch = t.blocks * kBK;
   CUtensorMap map_rows, map_w;
   {

@@ -18,7 +18,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import attn
-from .attn import _i32, _scratch
+from .attn import _i32
 from .moe import _TORCH2MOE, _check, _dt, lib
 
 _f32, _i8 = torch.float32, torch.int8
@@ -113,9 +113,12 @@ def linear_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
     m, n, out_row = _rows(out, dev)
     assert (m, n) == (M, N) and out.dtype in _TORCH2MOE
     L = lib()
-    ws = _scratch(L.moe_linear_w8a8_workspace_size(M, N, K), a)
-    _check(L.moe_linear_w8a8(a.data_ptr(), a_row, sa, w.data_ptr(), w_row, sw, b, M, N, K, out.data_ptr(), out_row, _dt(out),
-                             ws.data_ptr(), ws.numel(), _raw_stream(dev)), "moe_linear_w8a8")
+    wp = w.data_ptr()
+    whole = (K | w_row | wp) % 16 == 0                 # w is read where it is
+    size = L.moe_linear_w8a8_workspace_size(M, 0 if whole else N, K)
+    ws = torch.empty(size, dtype=torch.uint8, device=a.device) if size else None
+    _check(L.moe_linear_w8a8(a.data_ptr(), a_row, sa, wp, w_row, sw, b, M, N, K, out.data_ptr(), out_row, _dt(out),
+                             None if ws is None else ws.data_ptr(), size, _raw_stream(dev)), "moe_linear_w8a8")
     return out
 
 
