@@ -100,14 +100,13 @@ def test_neighbours_are_left_alone(dense):
 
 @pytest.mark.parametrize("dtype", TYPES)
 def test_a_row_does_not_depend_on_the_others(dense, dtype):
-    """Alone, in a few and in many rows a row of one start's alignment gives the same bits."""
-    x = draw(400, 1024, dtype, 5)
-    many = dense.rmsnorm(on(x), q8=True)
-    few = dense.rmsnorm(on(x[:20]), q8=True)
-    for a, b in ((many.y[:20], few.y), (many.q[:20], few.q), (many.scale[:20], few.scale)):
-        assert (a.double() - b.double()).abs().max() <= (1 if a.dtype is torch.int8 else float(a.abs().max()) * 2.0 ** -7)
-    again = dense.rmsnorm(on(x), q8=True)
-    assert torch.equal(again.y, many.y) and torch.equal(again.q, many.q) and torch.equal(again.scale, many.scale)
+    """Alone, among a few and among many rows: the same bits, on every run."""
+    for d in (96, 1024, 4096, 8200, 333):
+        x, r = draw(400, d, dtype, 5), draw(400, d, dtype, 6)
+        many = dense.rmsnorm(on(x), residual=on(r), q8=True)
+        for first, n in ((0, 1), (7, 20), (399, 1), (100, 300), (0, 400)):
+            part = dense.rmsnorm(on(x[first:first + n]), residual=on(r[first:first + n]), q8=True)
+            assert all(torch.equal(a[first:first + n], b) for a, b in zip(many, part))
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
