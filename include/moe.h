@@ -578,7 +578,7 @@ int moe_quantize_rows(const void *x, int64_t x_stride, int dtype, int64_t T, int
  *   acc = sum_k a[m, k] * w[n, k]   (exact, 32-bit),
  *   out[m, n] = RN((fp32(acc) * a_scale[m]) * w_scale[n] (+ bias[n]))   (fp32 operations in this order, each rounded).
  * a: int8 (M, K), w: int8 (N, K) (moe_quantize_rows gives either; every int8 value is taken), a_scale fp32 (M), w_scale
- * fp32 (N), bias fp32 (N) or NULL, out (M, N) F16 | BF16 | F32.  1 <= K <= 131071.  The result does not depend on M, on the
+ * fp32 (N), bias fp32 (N) or NULL, out (M, N) F16 | BF16 | F32, apart from the inputs.  1 <= K <= 131071.  The result does not depend on M, on the
  * other rows or on which kernel runs: a token's outputs are the same bits alone and in any batch.
  * workspace: >= moe_linear_w8a8_workspace_size(M, N, K) bytes; one sized for M serves every call of fewer rows with the same N
  * and K.  Its contents have no influence.  Rows of w that do not all start on 16 bytes (K % 16 != 0 among them) are copied into it

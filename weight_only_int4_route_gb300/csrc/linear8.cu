@@ -12,14 +12,20 @@
 namespace moe {
 namespace {
 
-// Rows of K bytes -> rows of `pitch` bytes, zeros behind: weights whose rows do not start on 16 bytes.
+// Rows of K bytes -> rows of `pitch` bytes, zeros behind: weights whose rows do not start on 16 bytes.  A thread per 16 bytes.
 __global__ void __launch_bounds__(256) pad_rows_kernel(const int8_t *w, int64_t stride, int64_t rows, int K, int pitch, int8_t *out) {
   pdl_enter();
-  const int64_t total = rows * pitch;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-    const int64_t r = i / pitch;
-    const int k = int(i - r * pitch);
-    out[i] = k < K ? w[r * stride + k] : int8_t(0);
+  const int per = pitch / 16;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * per; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = (i >> 32) == 0 ? int64_t(uint32_t(i) / uint32_t(per)) : i / per;
+    const int k = int(i - r * per) * 16;
+    const int8_t *src = w + r * stride + k;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    int8_t *byte = reinterpret_cast<int8_t *>(&v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (k + j < K) byte[j] = src[j];
+    *reinterpret_cast<uint4 *>(out + r * pitch + k) = v;
   }
 }
 
@@ -286,7 +292,7 @@ extern "C" int moe_linear_w8a8(const int8_t *a, int64_t a_stride, const float *a
   if (pad) {
     const int pitch = int((K + 15) & ~int64_t(15));
     int8_t *padded = static_cast<int8_t *>(workspace) + rows_bytes;
-    const int64_t blocks = std::min<int64_t>(cdiv(N * pitch, 256), int64_t(num_sms()) * 32);
+    const int64_t blocks = std::min<int64_t>(cdiv(N * (pitch / 16), 256), int64_t(num_sms()) * 32);
     launch_pdl(pad_rows_kernel, dim3(unsigned(blocks)), dim3(256), 0, st, w, p.w_stride, N, int(K), pitch, padded);
     MOE_TRY(check_launch("linear_w8a8 padding"));
     p.w = padded;

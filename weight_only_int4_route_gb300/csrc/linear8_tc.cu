@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(const int8_t *__restri
   const int per = pitch / 16;
   const int64_t total = M * per;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-    const int64_t r = i / per;
+    const int64_t r = (i >> 32) == 0 ? int64_t(uint32_t(i) / uint32_t(per)) : i / per;
     const int k = int(i - r * per) * 16;
     uint4 v = make_uint4(0, 0, 0, 0);
     const int8_t *src = a + r * stride + k;
