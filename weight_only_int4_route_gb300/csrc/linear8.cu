@@ -37,7 +37,8 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const int8_t *w, int64_t 
 // lane's 16 consecutive values stand for the slots that four MMAs want of it, and the rows' values, f16 in shared memory and
 // read the same way, match.  (m16n8k32 on the integers themselves takes 128 cycles a sub-core on this chip: one row of 4096 x 6144
 // 8.2 us, 16 rows 16.3 us.)  A warp's accumulators are emptied into the 32-bit integers after 1024 of K: up to there an
-// fp32 sum of these products is exact.
+// fp32 sum of these products is exact.  Measured on GB300: one row of 6144 x 4096 7.2 us, 3.5 TB/s, of 32768 x 2048 17.6 us, 3.8 TB/s; a
+// third of the first is launch, the rows' way to shared memory and the joining of the sums.
 constexpr int kStreamThreads = 256, kStreamWarps = 8, kStreamSmem = 72 * 1024;
 
 __device__ __forceinline__ uint4 load_stream(const int8_t *p) {

@@ -23,6 +23,12 @@
 //   warp 18      MMAs, one thread.
 // Few tiles: the CTAs of a cluster take a range of K each and add their integers up through distributed shared memory.
 //
+// Measured on GB300: 8192 x 6144 x 4096 281 us with the rows' conversion (15 us), 1.47 PFLOP/s, 0.85 of the sustained 16-bit rate; a K
+// block takes 1000 cycles, what shared memory needs.  300 x 6144 x 2048 18 us, 24 rows of 4096 x 4096 11.6 us: there a block takes
+// the MMA thread's 900 cycles (8 issues of 65, two waits, a commit), and 6 us are launches, first copies and the outputs.
+// Tried: W stages of half a K block, four of them (8192 rows 346 us at the time of 314: twice the waits and commits);
+// waits that test without suspending (no change).
+//
 // Every wait is bounded (see tc_ptx.cuh); on expiry the CTA records a code, stops, drains its copies and MMAs, frees
 // tensor memory and returns.
 #include <algorithm>

@@ -6,7 +6,10 @@
 // The factor r of a row is positive and common to it, so the 8-bit codes follow from u alone: the sum of squares and
 // the largest magnitude come out of one pass over the row, with one exchange between its warps.  A row stays in its
 // threads' registers between the loads and the stores, so memory sees every element once: the kernel is bound by it
-// (2 + 2 + 2 + 1 bytes an element for 16-bit rows with a residual and 8-bit output).
+// (2 + 2 + 2 + 1 bytes an element for 16-bit rows with a residual and 8-bit output).  Measured on GB300: 8192 rows of 4096 in
+// bf16, residual and 8-bit output, 39.8 us, 5.9 TB/s; 2501 rows of 2048 in f16, residual and 16-bit output, 6.9 us, 6.0 TB/s.
+// Blocks that walk over rows with the next one's loads in flight were slower (82 us at the time of 67): registers, not
+// loads, bounded the warps in flight.
 #include <type_traits>
 
 #include "moe_internal.cuh"
@@ -27,7 +30,7 @@ struct NormArgs {
 constexpr int kMaxD = 16384;
 
 // V elements of a row: 16 bytes, or one.  Words, not arrays of elements: those cost a permute for every element that is read
-// or put in (33 instructions an element in all, 9 now).
+// or put in (8192 rows of 4096 with residual and 8-bit output 60 us, 40 with words).
 template <typename T, int V> struct Pack {
   uint32_t w[4];
   __device__ __forceinline__ void load(const T *p) {

@@ -16,7 +16,9 @@
 // after the other.
 //
 // Few long rows are shared by the CTAs of a cluster, which send their sums and their k best to the first one.
-// Bound by memory for many rows, by the length of this chain for a few.
+// Bound by the instructions of a row's elements beside memory for many rows, by the length of this chain for a few.  Measured on
+// GB300 (k = 8 or 5): 4096 rows of 65521 in bf16 104 us, 5.2 TB/s (without alternatives 90 us; 6 waves of rows where 5.4 would
+// do); 320 rows of 131072 23.5 us; one row of 32000 in fp32 5.8 us, of which the alternatives are 2.
 #include <type_traits>
 
 #include "tc_ptx.cuh"
