@@ -20,12 +20,13 @@
 //   warps 8-15   conversion, two groups of four warps; K block i belongs to group i % 2 and W stage i % 2;
 //   warp 16, 17  copies of the rows (a ring of 3) and of W (a ring of 4: a multiple of the groups, so that a stage's
 //                fills all go to one group and a wait by parity cannot be a phase ahead);
-//   warp 18      MMAs, one thread.
+//   warp 18      MMAs, one thread;
+//   warp 19      passes the arrival of a block's rows on to the barrier of its W stage: the MMA thread has one wait a block.
 // Few tiles: the CTAs of a cluster take a range of K each and add their integers up through distributed shared memory.
 //
-// Measured on GB300: 8192 x 6144 x 4096 281 us with the rows' conversion (15 us), 1.47 PFLOP/s, 0.85 of the sustained 16-bit rate; a K
-// block takes 1000 cycles, what shared memory needs.  300 x 6144 x 2048 18 us, 24 rows of 4096 x 4096 11.6 us: there a block takes
-// the MMA thread's 900 cycles (8 issues of 65, two waits, a commit), and 6 us are launches, first copies and the outputs.
+// Measured on GB300: 8192 x 6144 x 4096 276 us with the rows' conversion (15 us), 1.50 PFLOP/s, 0.87 of the sustained 16-bit rate; a K
+// block takes 1000 cycles, what shared memory needs.  300 x 6144 x 2048 17.4 us, 24 rows of 4096 x 4096 11.6 us: there a block takes
+// the MMA thread's 850 cycles (8 issues of 65, a wait, a commit), and 6 us are launches, first copies and the outputs.
 // Tried: W stages of half a K block, four of them (8192 rows 346 us at the time of 314: twice the waits and commits);
 // waits that test without suspending (no change).
 //
@@ -55,7 +56,7 @@ int linear8_error_take(int *out) {
 namespace {
 
 constexpr int kEpiWarps = 8, kGroups = 2, kGroupWarps = 4;
-constexpr int kConvWarp = kEpiWarps, kRowWarp = kConvWarp + kGroups * kGroupWarps, kWeightWarp = kRowWarp + 1, kMmaWarp = kRowWarp + 2;
+constexpr int kConvWarp = kEpiWarps, kRowWarp = kConvWarp + kGroups * kGroupWarps, kWeightWarp = kRowWarp + 1, kMmaWarp = kRowWarp + 2, kRelayWarp = kRowWarp + 3;
 constexpr int kTcThreads = (kRowWarp + 4) * 32;   // whole warpgroups: registers are dealt by them
 constexpr int kEpiRegs = 144, kOtherRegs = 64;   // 256 x 144 + 384 x 64 = 640 x 96, all there are
 // CTAs of a cluster at most.  Clusters of 8 with this much shared memory do not all run at once (2048 x 2048, 24 rows: 12 us with 4,
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&wfree[s], kGroupWarps);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ready[s], kGroupWarps);
+      mbar_init(&ready[s], kGroupWarps + 1);
       mbar_init(&d_full[s], 1);
       mbar_init(&d_empty[s], kEpiWarps);
     }
@@ -321,14 +322,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       for (uint32_t n = it > kWStages ? it - kWStages : 0; n < it; ++n)
         mbar_wait(&wfull[n % kWStages], (n / kWStages) & 1, &never, kErrDrain, &g_linear8_error);
+    } else if (warp == kRelayWarp && lane == 0) {
+      // ------------------------------------------------ rows landed -> ready
+      // A block's rows land again only after its MMAs, which wait for this: no phase can be missed.
+      uint32_t it = 0;
+      bool ok = true;
+      for (int i = tile0; ok && i < tiles; i += step)
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          if (!(ok = wait(&rfull[it % kRowStages], it / kRowStages, kErrFull))) break;
+          mbar_arrive(&ready[it % kGroups]);
+        }
     } else if (warp == kMmaWarp && lane == 0) {
       // ------------------------------------------------ MMAs
       // One thread's path bounds the kernel, so its state is kept in registers: shared-memory addresses, stages and parities
       // that are stepped, not divided out.
       const uint32_t idesc = idesc_f16(0, kBM, t.rows);
-      const uint32_t b_rfull = su32(rfull), b_done = su32(done), b_ready = su32(ready), b_dfull = su32(d_full), b_dempty = su32(d_empty);
+      const uint32_t b_done = su32(done), b_ready = su32(ready), b_dfull = su32(d_full), b_dempty = su32(d_empty);
       const uint64_t rows0 = sw128_desc(su32(s_row));
-      uint32_t s = 0, s_par = 0, w = 0, w_par = 0, d = 0, d_par = 1;
+      uint32_t s = 0, w = 0, w_par = 0, d = 0, d_par = 1;
       auto wait_at = [&](uint32_t b, uint32_t parity, int code) { return mbar_wait_at(b, parity, abort_flag, code, &g_linear8_error); };
       bool ok = true;
       for (int i = tile0; ok && i < tiles; i += step) {
@@ -337,11 +348,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (!(ok = wait_at(b_dempty + 8 * d, d_par, kErrD))) break;
           const uint32_t acc = tmem + d * kBN;
           for (int kb = 0; kb < n; ++kb) {
-            if (!(ok = wait_at(b_rfull + 8 * s, s_par, kErrFull) && wait_at(b_ready + 8 * w, w_par, kErrReady))) break;
+            if (!(ok = wait_at(b_ready + 8 * w, w_par, kErrReady))) break;
             tc_fence_after();
             tc_mma_kblock_ts<kHalf / 16, false>(acc, tmem + kACol0 + w * kACols, rows0 + s * (kRowBytes / 16), idesc, uint32_t(kb));
             tc_commit_at(b_done + 8 * s);
-            if (++s == kRowStages) s = 0, s_par ^= 1;
+            if (++s == kRowStages) s = 0;
             w_par ^= w;
             w ^= 1;
           }

@@ -50,7 +50,8 @@ def _device(t: torch.Tensor) -> int:
 def _rows(t: torch.Tensor, dev: int):
     """(rows, row length, row stride) of a tensor whose rows are contiguous."""
     assert t.get_device() == dev, "a call's tensors are on one GPU"
-    (n, d), (row, one) = t.shape, t.stride()
+    n, d = t.shape
+    row, one = t.stride()
     assert one == 1 or d == 1, "a row's elements lie side by side"
     return n, d, row if n > 1 else d       # torch leaves the stride of a dimension of one open
 
@@ -67,23 +68,28 @@ def rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float =
     With a residual the sum is returned too, in sum_out if given (which may be residual or x itself)."""
     dev = _device(x)
     T, d, xs = _rows(x, dev)
-    rp = rs = sp = ss = None
-    total = None
+    rp = sp = yp = qp = cp = total = out = q = scale = None
+    rs = ss = 0
+    where = x.device
     if residual is not None:
         assert residual.shape == x.shape and residual.dtype is x.dtype
         rp, rs = residual.data_ptr(), _rows(residual, dev)[2]
-        total = torch.empty((T, d), dtype=x.dtype, device=x.device) if sum_out is None else sum_out
-        assert total.shape == x.shape and total.dtype is x.dtype
-        sp, ss = total.data_ptr(), _rows(total, dev)[2]
+        if sum_out is None:
+            total, ss = torch.empty((T, d), dtype=x.dtype, device=where), d
+        else:
+            total, ss = sum_out, _rows(sum_out, dev)[2]
+            assert total.shape == x.shape and total.dtype is x.dtype
+        sp = total.data_ptr()
     else:
         assert sum_out is None, "sum_out comes with a residual"
     wp = None if weight is None else _vector(weight, dev, d, x.dtype)
-    out = torch.empty((T, d), dtype=x.dtype, device=x.device) if y else None
-    q = scale = None
+    if y:
+        out = torch.empty((T, d), dtype=x.dtype, device=where)
+        yp = out.data_ptr()
     if q8:
-        q, scale = torch.empty((T, d), dtype=_i8, device=x.device), torch.empty(T, dtype=_f32, device=x.device)
-    _check(lib().moe_rmsnorm(x.data_ptr(), xs, rp, rs or 0, wp, _dt(x), T, d, eps, sp, ss or 0, out.data_ptr() if y else None,
-                             q.data_ptr() if q8 else None, scale.data_ptr() if q8 else None, _raw_stream(dev)), "moe_rmsnorm")
+        q, scale = torch.empty((T, d), dtype=_i8, device=where), torch.empty(T, dtype=_f32, device=where)
+        qp, cp = q.data_ptr(), scale.data_ptr()
+    _check(lib().moe_rmsnorm(x.data_ptr(), xs, rp, rs, wp, _dt(x), T, d, eps, sp, ss, yp, qp, cp, _raw_stream(dev)), "moe_rmsnorm")
     return Normed(out, q, scale, total)
 
 
@@ -109,9 +115,11 @@ def linear_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
     sa, sw = _vector(a_scale, dev, M, _f32), _vector(w_scale, dev, N, _f32)
     b = None if bias is None else _vector(bias, dev, N, _f32)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
-    m, n, out_row = _rows(out, dev)
-    assert (m, n) == (M, N) and out.dtype in _TORCH2MOE
+        out, out_row = torch.empty((M, N), dtype=out_dtype, device=a.device), N
+    else:
+        m, n, out_row = _rows(out, dev)
+        assert (m, n) == (M, N)
+    assert out.dtype in _TORCH2MOE
     L = lib()
     wp = w.data_ptr()
     whole = (K | w_row | wp) % 16 == 0                 # w is read where it is
@@ -134,12 +142,13 @@ def token_logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None, k: 
         assert ids.dim() in (1, 2) and ids.shape[0] == T
         shape = ids.shape
         n, ip = (1 if ids.dim() == 1 else shape[1]), ids.data_ptr()
-    new = dict(dtype=_f32, device=logits.device)
-    logprob, entropy, lse = torch.empty(shape, **new), torch.empty(T, **new), torch.empty(T, **new)
-    top_ids = top = None
+    where = logits.device
+    logprob, entropy = torch.empty(shape, dtype=_f32, device=where), torch.empty(T, dtype=_f32, device=where)
+    lse = torch.empty_like(entropy)
+    top_ids = top = tp = lp = None
     if k > 0:
-        top_ids, top = torch.empty((T, k), dtype=_i32, device=logits.device), torch.empty((T, k), **new)
+        top_ids, top = torch.empty((T, k), dtype=_i32, device=where), torch.empty((T, k), dtype=_f32, device=where)
+        tp, lp = top_ids.data_ptr(), top.data_ptr()
     _check(lib().moe_token_logprobs(logits.data_ptr(), row, _dt(logits), T, V, scale, ip, n, logprob.data_ptr(), entropy.data_ptr(),
-                                    lse.data_ptr(), k, None if k <= 0 else top_ids.data_ptr(), None if k <= 0 else top.data_ptr(),
-                                    _raw_stream(dev)), "moe_token_logprobs")
+                                    lse.data_ptr(), k, tp, lp, _raw_stream(dev)), "moe_token_logprobs")
     return Scores(logprob, entropy, lse, top_ids, top)
