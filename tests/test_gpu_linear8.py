@@ -159,3 +159,32 @@ def test_captured_and_replayed(dense, M):
         x.copy_(torch.roll(x, 1, 0) if bool(x.any()) else a)
         graph.replay()
         assert torch.equal(out, dense.linear_w8a8(x, sa, w, sw, b))
+
+
+def test_results_past_32_bits(dense):
+    """More results than 2^31: rows at the end are what they are in a small batch."""
+    M, N, K = 70001, 32000, 64
+    g = torch.Generator(device=DEV).manual_seed(5)
+    a = torch.randint(-128, 128, (M, K), generator=g, device=DEV, dtype=torch.int16).to(I8)
+    w = torch.randint(-128, 128, (N, K), generator=g, device=DEV, dtype=torch.int16).to(I8)
+    sa, sw = torch.rand(M, generator=g, device=DEV), torch.rand(N, generator=g, device=DEV)
+    whole = dense.linear_w8a8(a, sa, w, sw)
+    for first in (0, 35000, M - 9):
+        part = dense.linear_w8a8(a[first:first + 9], sa[first:first + 9].clone(), w, sw)
+        assert torch.equal(part, whole[first:first + 9])
+    assert same(part, D.linear_w8a8(a[-9:].cpu(), sa[-9:].cpu(), w.cpu(), sw.cpu(), None, torch.bfloat16))
+
+
+@pytest.mark.parametrize("M,N,K", [(190, 19456, 384), (64, 8192, 1536), (1000, 2048, 640)])
+def test_many_launches_agree(dense, M, N, K):
+    """Hundreds of launches with everything of a CTA's pipeline at its start: rows in memory before weights are converted, other
+    weights each time."""
+    sets = [tuple(t.to(DEV) for t in draw(M, N, K, seed)[:4]) for seed in range(4)]
+    refs = [dense.linear_w8a8(a, sa, w, sw, out_dtype=torch.float32) for a, sa, w, sw in sets]
+    few = [dense.linear_w8a8(a[:16], sa[:16].clone(), w, sw, out_dtype=torch.float32) for a, sa, w, sw in sets]    # another kernel
+    assert all(torch.equal(r[:16], f) for r, f in zip(refs, few))
+    bad = torch.zeros((), dtype=torch.int64, device=DEV)
+    for i in range(400):
+        a, sa, w, sw = sets[i % 4]
+        bad += (dense.linear_w8a8(a, sa, w, sw, out_dtype=torch.float32) != refs[i % 4]).sum()
+    assert int(bad) == 0

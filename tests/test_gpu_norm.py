@@ -182,3 +182,13 @@ def test_rows_past_32_bits(dense):
     q, s = dense.quantize_rows(wide[:, :d])
     rq, rs = D.quantize_rows(x)
     assert torch.equal(q.cpu(), rq) and torch.equal(s.cpu(), rs)
+
+
+def test_elements_past_32_bits(dense):
+    T, d = 140001, 16384
+    x = torch.randn((T, d), dtype=torch.bfloat16, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    n = dense.rmsnorm(x, q8=True)
+    for first in (0, 70000, T - 3):
+        part = dense.rmsnorm(x[first:first + 3], q8=True)
+        assert torch.equal(part.y, n.y[first:first + 3]) and torch.equal(part.q, n.q[first:first + 3])
+        check(part, x[first:first + 3].cpu(), None, None, 1e-6)

@@ -205,3 +205,13 @@ def test_runs_agree_bit_for_bit_and_replay(dense):
             graph.replay()
             again = dense.token_logprobs(x, ids, k=20)
             assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(first, again, held))
+
+
+def test_many_short_rows(dense):
+    x, ids = draw(200001, 33, torch.bfloat16, 4)
+    s = dense.token_logprobs(x.to(DEV), ids.to(DEV), k=3)
+    few = torch.tensor([0, 1, 65535, 65536, 131071, 200000])
+    lp = D.token_logprobs(x[few], ids[few], 3)
+    assert torch.equal(s.top_ids[few].cpu(), lp[3])
+    check(dense, x[few], ids[few], 3)
+    assert torch.equal(s.logprob[few], dense.token_logprobs(x[few].to(DEV), ids[few].to(DEV), k=3).logprob)

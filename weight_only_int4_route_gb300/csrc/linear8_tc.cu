@@ -24,7 +24,7 @@
 //   warp 19      passes the arrival of a block's rows on to the barrier of its W stage: the MMA thread has one wait a block.
 // Few tiles: the CTAs of a cluster take a range of K each and add their integers up through distributed shared memory.
 //
-// Measured on GB300: 8192 x 6144 x 4096 276 us with the rows' conversion (15 us), 1.50 PFLOP/s, 0.87 of the sustained 16-bit rate; a K
+// Measured on GB300: 8192 x 6144 x 4096 279 us with the rows' conversion (15 us), 1.48 PFLOP/s, 0.85 of the sustained 16-bit rate; a K
 // block takes 1000 cycles, what shared memory needs.  300 x 6144 x 2048 17.4 us, 24 rows of 4096 x 4096 11.6 us: there a block takes
 // the MMA thread's 850 cycles (8 issues of 65, a wait, a commit), and 6 us are launches, first copies and the outputs.
 // Tried: W stages of half a K block, four of them (8192 rows 346 us at the time of 314: twice the waits and commits);
@@ -324,12 +324,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_wait(&wfull[n % kWStages], (n / kWStages) & 1, &never, kErrDrain, &g_linear8_error);
     } else if (warp == kRelayWarp && lane == 0) {
       // ------------------------------------------------ rows landed -> ready
-      // A block's rows land again only after its MMAs, which wait for this: no phase can be missed.
+      // Up to three blocks' rows land ahead of the conversion: one is passed on only when the MMAs two blocks before are complete,
+      // or it would count in that block's phase of the barrier.  Rows land again only after their block's MMAs, which wait
+      // for this: no phase can be missed.
       uint32_t it = 0;
       bool ok = true;
       for (int i = tile0; ok && i < tiles; i += step)
         for (int kb = 0; kb < nkb; ++kb, ++it) {
-          if (!(ok = wait(&rfull[it % kRowStages], it / kRowStages, kErrFull))) break;
+          ok = wait(&rfull[it % kRowStages], it / kRowStages, kErrFull) &&
+               (it < 2 || wait(&done[(it - 2) % kRowStages], (it - 2) / kRowStages, kErrFree));
+          if (!ok) break;
           mbar_arrive(&ready[it % kGroups]);
         }
     } else if (warp == kMmaWarp && lane == 0) {
