@@ -125,6 +125,19 @@ def test_large_and_small_values(dense, dtype):
     assert n.scale[4] == 0 and (n.q[4] == 0).all() and (n.y[4] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 2048])
+def test_no_eps(dense, dtype, d):
+    """Without an eps rows of any size are normalised, squares below fp32's numbers included; a row of zeros is 0 / 0."""
+    x = draw(5, d, dtype, 19) * torch.tensor([[1.0], [2.0 ** -40], [2.0 ** -64], [2.0 ** -100], [0.0]]).to(dtype)
+    n = dense.rmsnorm(on(x), None, 0.0, q8=True)
+    v = D.rmsnorm(x, None, None, 0.0)[1]
+    steps, scale = D.steps8(torch.nan_to_num(v))
+    assert ((n.y.double().cpu() - v).abs() <= (U[dtype] + 48 * E) * v.abs())[:4].all() and torch.isnan(n.y[4]).all()
+    assert ((n.scale.double().cpu() - scale).abs() <= 48 * E * scale).all()
+    assert ((n.q.double().cpu() - steps).abs() <= 0.5 + 127 * 6 * E).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("d", [64, 2048, 77])

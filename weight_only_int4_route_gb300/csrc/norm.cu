@@ -181,12 +181,15 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs p) {
   };
   reduce();
   if (p.norm) {
-    if (isinf(ss)) {   // squares past fp32 (magnitudes above 1.8e19): the row again, 2^-64 times as large
-      eps *= 0x1p-128f;
+    // squares past fp32's range (magnitudes above 1.8e19), or below it with an eps that does not cover them: the row again, a power
+    // of two times as large
+    const float by = isinf(ss) ? 0x1p-64f : (fmaf(ss, p.inv_d, eps) < 0x1p-96f ? 0x1p64f : 1.f);
+    if (by != 1.f) {
+      eps = eps * by * by;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) h[i][j] *= 0x1p-64f;
+        for (int j = 0; j < V; ++j) h[i][j] *= by;
       reduce();
     }
     r = rsqrtf(fmaf(ss, p.inv_d, eps));
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs p) {
       for (int j = 0; j < V; ++j) c[j] = fine ? __float_as_uint(__fadd_rn(__fmul_rn(h[i][j] * f[j], step), 12582912.f)) : 0;
       if (at(i) < p.d) P::store_codes(q + at(i), c);
     }
-    if (t == 0) p.scale[row] = fine ? __fdiv_rn(top, 127.f) * r : __int_as_float(0x7fc00000);
+    if (t == 0) p.scale[row] = !fine ? __int_as_float(0x7fc00000) : (top > 0.f ? __fdiv_rn(top, 127.f) * r : 0.f);
   }
 }
 
