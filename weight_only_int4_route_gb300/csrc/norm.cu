@@ -7,7 +7,7 @@
 // the largest magnitude come out of one pass over the row, with one exchange between its warps.  A row stays in its
 // threads' registers between the loads and the stores, so memory sees every element once: the kernel is bound by it
 // (2 + 2 + 2 + 1 bytes an element for 16-bit rows with a residual and 8-bit output).  Measured on GB300: 8192 rows of 4096 in
-// bf16, residual and 8-bit output, 39.8 us, 5.9 TB/s; 2501 rows of 2048 in f16, residual and 16-bit output, 6.9 us, 6.0 TB/s.
+// bf16, residual and 8-bit output, 40.1 us, 5.9 TB/s; 2501 rows of 2048 in f16, residual and 16-bit output, 6.9 us, 6.0 TB/s.
 // Blocks that walk over rows with the next one's loads in flight were slower (82 us at the time of 67): registers, not
 // loads, bounded the warps in flight.
 #include <type_traits>
@@ -252,7 +252,7 @@ template <typename T, int V> int launch_rows(NormArgs p, cudaStream_t st) {
   } else {
     // 32 elements a thread (fp32: 16) whatever the number of rows: a row's sum has one order, its result is the same in every
     // batch.  8192 rows of 4096: 8, 16 and 32 elements a thread 70, 43 and 40 us; 8 rows 2.4 us with
-    // 8 and with 32.
+    // 8 and 2.7 with 32.
     if (vecs <= 512 * 4) return go(integral_constant<int, 4>{}, integral_constant<int, 512>{});
     if constexpr (V == 4) return go(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
     return set_error(MOE_ERR_UNSUPPORTED, "rows of at most %d elements", kMaxD);
