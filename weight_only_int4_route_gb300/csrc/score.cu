@@ -1,13 +1,13 @@
 // Log probabilities of given tokens, entropy and top alternatives of rows of logits.
 //
 // With z_j = scale * x_j:  lse = ln sum_j exp z_j,  logprob_t = z_t - lse,  entropy = lse - sum_j p_j z_j.
-// One pass over the row: every thread keeps a reference M, Z = sum exp(scale (x - M)) and S = sum exp(scale (x - M)) (x - M).  M
+// One pass over the row: every thread keeps a reference M, Z = sum 2^t and S = sum 2^t t, t = (x - M) c, c = scale log2(e).  M
 // starts as the largest logit of the warp's first loads and follows only what is above it by more than 2^6 in weight (Z' = Z f,
-// S' = f (S + d Z), f = exp(scale d), d = M - M'): a reference that followed every new largest logit would move in some
-// lane of a warp at nearly every step.  entropy = ln Z - scale S / Z, and with M within 2^6 of the row's largest no digits cancel
+// S' = f (S + d Z), f = 2^d, d = (M - M') c): a reference that followed every new largest logit would move in some
+// lane of a warp at nearly every step.  entropy = ln Z - ln 2 S / Z, and with M within 2^6 of the row's largest no digits cancel
 // but those that a factor of 64 is worth (ln 64 = 4.2 beside an entropy of up to ln V).
 // An element costs a conversion, half a maximum and half a clamp (in pairs, in its own type), a 2^x and three fp32 operations:
-// the exponent is x c - fl(M c), c = scale log2(e), and what the rounding of M c put in is taken out of the sums at the end.
+// the exponent is x c - fl(M c), and what the rounding of M c put in is taken out of the sums at the end.
 //
 // Top alternatives, in the order of (logit descending, id ascending): a thread knows its largest logit.  A value `from` is
 // found, by halving intervals, that at least k threads and few more reach with theirs: the k best are at or above it, and only
@@ -31,7 +31,7 @@ constexpr int kResident = 5;        // blocks of an SM (51 registers a thread; w
 constexpr int kMaxK = 64;
 constexpr int kCand = 1024;         // elements collected at most
 constexpr int kMaxParts = 8;        // CTAs of a row (the portable cluster size)
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct ScoreArgs {
   const void *x;
@@ -113,14 +113,17 @@ template <bool CLAMP = false> __device__ __forceinline__ float open(const uint4 
   return top;
 }
 
-// Sums of a set of elements: largest logit m (NaN if any element is), reference M, Z and S.
+// Sums of a set of elements: largest logit m (NaN if any element is), reference M, Z and S.  S is in units of the exponent: in
+// units of x it would pass fp32's range under small scales.
 struct alignas(16) Sums {
   float m, M, z, s;
 };
+// (x - M) c.  x - M alone may pass fp32's range, the difference of their halves does not.
+__device__ __forceinline__ float exponent(float x, float M, float c) { return __fmul_rn(fmaf(-0.5f, M, 0.5f * x), c) * 2.f; }
 // z and s moved to reference M.  Nothing is left where the factor is 0 (0 times an infinite difference would be NaN) or where
 // nothing was (z = 0, whose reference does not count).
 __device__ __forceinline__ void move_to(float M, float c, const Sums &o, float &z, float &s) {
-  const float d = o.M - M, f = ex2(__fmul_rn(d, c));
+  const float d = exponent(o.M, M, c), f = ex2(d);
   const bool any = f != 0.f && o.z != 0.f;
   z = any ? o.z * f : 0.f;
   s = any ? f * fmaf(d, o.z, o.s) : 0.f;
@@ -232,27 +235,27 @@ __global__ void __launch_bounds__(kThreads, kResident) score_kernel(const ScoreA
   if (from < v1) batch(from, std::false_type{});
   if (has_head) one(tid);
   if (has_tail) one(tail_id);
-  // t was short of (x - M) c by Mc - M c, the product's rounding; then zs in units of x
+  // t was short of (x - M) c by Mc - M c, the product's rounding
   const float off = fmaf(M, c, -Mc), g = ex2(-off);
   z *= g;
-  zs = fmaf(zs, g, -off * z) / c;
+  zs = fmaf(zs, g, -off * z);
   if (m == -INFINITY) z = zs = 0.f;
   // Masked elements may have had weight (largest logits near the type's lowest, small scales), products been infinite, or the rounding
   // of M c been past the half unit that |M c| < 2^24 means (from 2^31 on t overflows): again, with differences that are
   // clamped.  A thread whose largest is nothing beside its warp's has nothing to add: a row masked by a large finite value is
   // read once more only where a warp sees nothing else (2048 rows of 32000 in bf16, one token in 20 not masked 36.7 us, one in
-  // 2000 43; deciding by the CTA's largest costs registers: 4096 rows of 65521 104 us and 112).  M c again and not Mc: that
+  // 2000 45; deciding by the CTA's largest costs registers: 4096 rows of 65521 104 us and 112).  M c again and not Mc: that
   // would be one register more in the loop (107 us).
   const bool poor = fabsf(m) < INFINITY && !((lowest(T()) - M) * c < -200.f && fabsf(__fmul_rn(M, c)) < 0x1p24f && c > 0x1p-40f && c < 64.f);
   const float most = value_of(__reduce_max_sync(0xffffffffu, ordered(m)));   // the warp's (see below for NaN)
   if (poor) {
     z = zs = 0.f;
     M = m;
-    const bool nothing = (m - most) * c < -200.f;
+    const bool nothing = exponent(m, most, c) < -200.f;
     auto again = [&](float e) {
-      const float d = fmaxf(e - M, -3.402823466e38f), w = ex2(__fmul_rn(d, c));
+      const float t = fmaxf(exponent(e, M, c), -1000.f), w = ex2(t);   // -inf: a weight of 0 under any scale
       z += w;
-      zs = fmaf(w, d, zs);
+      zs = fmaf(w, t, zs);
     };
     for (int v = nothing ? v1 : v0 + tid; v < v1; v += kThreads) {
       float e[VE];
@@ -439,7 +442,9 @@ __global__ void __launch_bounds__(kThreads, kResident) score_kernel(const ScoreA
     if (u.m != u.m) return nan;
     if (u.m == -INFINITY) return -INFINITY;
     if (u.m == INFINITY) return e == INFINITY ? nan : -INFINITY;
-    return fmaf(e - u.M, p.scale, -lz);
+    const float d = e - u.M;
+    if (isinf(d) && !isinf(e)) return fmaf(__fmul_rn(0.5f * e - 0.5f * u.M, p.scale), 2.f, -lz);   // further apart than fp32 reaches
+    return fmaf(d, p.scale, -lz);
   };
   if (tid < p.n_ids) p.logprob[asked] = id >= 0 && id < p.V ? logprob(logit) : nan;
   for (int i = tid + kThreads; i < p.n_ids; i += kThreads) {
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, kResident) score_kernel(const ScoreA
   if (tid == 0) {
     const bool finite = fabsf(u.m) < INFINITY;
     if (p.lse) p.lse[row] = finite ? fmaf(u.M, p.scale, lz) : u.m;
-    if (p.entropy) p.entropy[row] = finite ? fmaf(-p.scale, u.s / u.z, lz) : (u.m == -INFINITY ? 0.f : nan);
+    if (p.entropy) p.entropy[row] = finite ? fmaf(-kLn2, u.s / u.z, lz) : (u.m == -INFINITY ? 0.f : nan);
   }
   const int there = u.m == u.m ? min(p.k, p.V) : 0;
   for (int i = tid; i < PARTS * p.k; i += kThreads) {
