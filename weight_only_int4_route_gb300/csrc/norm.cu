@@ -182,8 +182,9 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs p) {
   reduce();
   if (p.norm) {
     // squares past fp32's range (magnitudes above 1.8e19), or below it with an eps that does not cover them: the row again, a power
-    // of two times as large.  2^-72: 16384 squares of at most (2^128 2^-72)^2 are within range.
-    const float by = isinf(ss) ? 0x1p-72f : (fmaf(ss, p.inv_d, eps) < 0x1p-96f ? 0x1p64f : 1.f);
+    // of two times as large.  2^-72: 16384 squares of at most (2^128 2^-72)^2 are within range.  2^96: the
+    // smallest subnormal number's square becomes 2^-106; these rows' elements are below 2^-41.
+    const float by = isinf(ss) ? 0x1p-72f : (fmaf(ss, p.inv_d, eps) < 0x1p-96f ? 0x1p96f : 1.f);
     if (by != 1.f) {
       eps = eps * by * by;
 #pragma unroll
