@@ -561,8 +561,8 @@ int moe_attention(const moe_kv_desc *desc, const moe_kv *kv, int64_t layer, cons
  * each written unless NULL.  A row of zeros gets q = 0 and q_scale = 0; one that holds a NaN or an infinity, or whose values
  * times weight pass fp32, gets q = 0 and q_scale = NaN, so that every product with it is NaN (y follows the
  * formula).  x, residual, weight, sum, y: dtype F16 | BF16 | F32; q: int8 (T, d); q_scale: fp32 (T); y and q contiguous.
- * A row's results do not depend on T or on the other rows, only on whether rows are read 16 bytes at a time (all of x,
- * residual and sum start on 16 bytes, with strides and d that are multiples of that) or element by element.
+ * A row's results depend neither on T nor on the other rows nor on where the rows lie; rows are read 16 bytes at a time if all of x,
+ * residual and sum start on 16 bytes, with strides and d that are multiples of that, else element by element.
  * 1 <= d <= 16384, eps >= 0.  sum may be x or residual itself with the same stride (in place); outputs must not overlap
  * inputs or each other otherwise.
  * moe_quantize_rows: q and q_scale of v = x, d <= 16384.

@@ -25,9 +25,11 @@ struct NormArgs {
   float *scale;
   float eps, inv_d;
   int d, lanes, norm;   // lanes: threads of a row (a multiple of 32)
+  int vector_lanes;     // those that a row of this size has where it is read 16 bytes at a time
 };
 
 constexpr int kMaxD = 16384;
+constexpr int kVectors = 4;   // 16-byte vectors of a thread
 
 // V elements of a row: 16 bytes, or one.  Words, not arrays of elements: those cost a permute for every element that is read
 // or put in (8192 rows of 4096 with residual and 8-bit output 60 us, 40 with words).
@@ -111,10 +113,15 @@ __device__ __forceinline__ void row_reduce(float &ss, float &top, int lanes, Exc
 }
 
 // A row per `lanes` threads, NV vectors of V elements a thread; Q8: with 8-bit output.
-template <typename T, int V, int NV, int MOST, bool Q8>
+// SV (with V = 1): rows that could be read 16 bytes, SV elements, at a time if they lay otherwise.  Their squares are added up in the
+// order that they have there (from shared memory, in fp32), so a row's result does not depend on where it lies.  In bf16 with
+// residual and 8-bit output: 8192 rows of 4096 at odd starts 121 us (16-byte starts 40), 5000 rows of 256 6.5 us (an
+// order of their own 5.8).
+template <typename T, int V, int NV, int MOST, bool Q8, int SV>
 __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs p) {
   pdl_enter();
   __shared__ Exchange exchange;
+  extern __shared__ __align__(16) float s_h[];
   using P = Pack<T, V>;
   const int rows = blockDim.x / p.lanes, t = int(threadIdx.x) % p.lanes;
   const int64_t row = int64_t(blockIdx.x) * rows + int(threadIdx.x) / p.lanes;
@@ -173,8 +180,29 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs p) {
       if (Q8) w[i].widen(f);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        ss = fmaf(h[i][j], h[i][j], ss);
+        if (SV == 0) ss = fmaf(h[i][j], h[i][j], ss);
         if (Q8) top = max_nan(top, fabsf(h[i][j] * f[j]));
+      }
+    }
+    if (SV > 0 && p.norm) {
+      float *s = s_h + int(threadIdx.x) / p.lanes * p.d;
+      __syncwarp();   // a second sum: the first one's values have been read (by other warps before row_reduce's barrier)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (at(i) < p.d) s[at(i)] = h[i][0];
+      if (p.lanes == 32) __syncwarp();
+      else __syncthreads();
+      if (t < p.vector_lanes) {
+        for (int k = t * SV; k < p.d; k += p.vector_lanes * SV) {
+#pragma unroll
+          for (int j = 0; j < SV; j += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(s + k + j);
+            ss = fmaf(v.x, v.x, ss);
+            ss = fmaf(v.y, v.y, ss);
+            ss = fmaf(v.z, v.z, ss);
+            ss = fmaf(v.w, v.w, ss);
+          }
+        }
       }
     }
     row_reduce(ss, top, p.lanes, exchange, turn);
@@ -236,14 +264,21 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs p) {
   }
 }
 
-template <typename T, int V> int launch_rows(NormArgs p, cudaStream_t st) {
+template <typename T, int V, int SV> int launch_rows(NormArgs p, cudaStream_t st) {
   const int vecs = (p.d + V - 1) / V;
   auto go = [&](auto nv, auto most) {
     constexpr int NV = decltype(nv)::value, MOST = decltype(most)::value;
     p.lanes = int(cdiv(cdiv(vecs, NV), 32) * 32);
     const int rows = p.lanes == 32 ? 4 : 1;
-    launch_pdl(p.q ? norm_kernel<T, V, NV, MOST, true> : norm_kernel<T, V, NV, MOST, false>, dim3(unsigned(cdiv(p.T, rows))),
-               dim3(unsigned(rows * p.lanes)), 0, st, p);
+    auto kernel = p.q ? norm_kernel<T, V, NV, MOST, true, SV> : norm_kernel<T, V, NV, MOST, false, SV>;
+    size_t smem = 0;
+    if constexpr (SV > 0) {
+      p.vector_lanes = int(cdiv(cdiv(p.d / SV, kVectors), 32) * 32);
+      smem = size_t(rows) * p.d * sizeof(float);
+      if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxD * sizeof(float))) != cudaSuccess)
+        return check_launch("rmsnorm attribute");
+    }
+    launch_pdl(kernel, dim3(unsigned(cdiv(p.T, rows))), dim3(unsigned(rows * p.lanes)), smem, st, p);
     return check_launch("rmsnorm");
   };
   using std::integral_constant;
@@ -254,18 +289,19 @@ template <typename T, int V> int launch_rows(NormArgs p, cudaStream_t st) {
     // 32 elements a thread (fp32: 16) whatever the number of rows: a row's sum has one order, its result is the same in every
     // batch.  8192 rows of 4096: 8, 16 and 32 elements a thread 70, 43 and 40 us; 8 rows 2.4 us with
     // 8 and 2.7 with 32.
-    if (vecs <= 512 * 4) return go(integral_constant<int, 4>{}, integral_constant<int, 512>{});
-    if constexpr (V == 4) return go(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
+    using Vectors = integral_constant<int, kVectors>;
+    if (vecs <= 512 * kVectors) return go(Vectors{}, integral_constant<int, 512>{});
+    if constexpr (V == 4) return go(Vectors{}, integral_constant<int, 1024>{});
     return set_error(MOE_ERR_UNSUPPORTED, "rows of at most %d elements", kMaxD);
   }
 }
 
 template <typename T> int launch_norm(const NormArgs &p, cudaStream_t st) {
   constexpr int V = 16 / int(sizeof(T));
-  auto whole = [](const void *q, int64_t stride) { return q == nullptr || (aligned16(q) && stride % V == 0); };
-  if (p.d % V == 0 && whole(p.x, p.x_stride) && whole(p.residual, p.residual_stride) && whole(p.sum, p.sum_stride))
-    return launch_rows<T, V>(p, st);
-  return launch_rows<T, 1>(p, st);
+  auto whole = [&](const void *q, int64_t stride) { return q == nullptr || (aligned16(q) && (stride % V == 0 || p.T == 1)); };
+  if (p.d % V != 0) return launch_rows<T, 1, 0>(p, st);
+  if (whole(p.x, p.x_stride) && whole(p.residual, p.residual_stride) && whole(p.sum, p.sum_stride)) return launch_rows<T, V, 0>(p, st);
+  return launch_rows<T, 1, V>(p, st);
 }
 
 int run_norm(const NormArgs &p, int dtype, cudaStream_t st) {
@@ -303,7 +339,7 @@ extern "C" int moe_rmsnorm(const void *x, int64_t x_stride, const void *residual
   MOE_REQUIRE(sum != x || sum_stride == x_stride || T == 1, "in place needs the same strides");
   MOE_REQUIRE(sum == nullptr || sum != residual || sum_stride == residual_stride || T == 1, "in place needs the same strides");
   NormArgs p{x, residual, weight, x_stride, residual_stride, sum_stride, T, sum, y, q, q_scale, eps, float(1.0 / double(d)),
-             int(d), 0, 1};
+             int(d), 0, 1, 0};
   return run_norm(p, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -314,6 +350,6 @@ extern "C" int moe_quantize_rows(const void *x, int64_t x_stride, int dtype, int
   if (T == 0) return MOE_OK;
   MOE_REQUIRE(x && on_element(x, dtype) && q && q_scale, "null or misaligned pointer");
   MOE_REQUIRE(aligned16(q) && aligned16(q_scale), "pointers must be 16-byte aligned");
-  NormArgs p{x, nullptr, nullptr, x_stride, 0, 0, T, nullptr, nullptr, q, q_scale, 0.f, 0.f, int(d), 0, 0};
+  NormArgs p{x, nullptr, nullptr, x_stride, 0, 0, T, nullptr, nullptr, q, q_scale, 0.f, 0.f, int(d), 0, 0, 0};
   return run_norm(p, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
