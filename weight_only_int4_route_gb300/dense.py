@@ -9,7 +9,8 @@ enqueued on torch's current stream.  A call's tensors are all on the current GPU
     logits = linear_w8a8(n.q, n.scale, head, head_scale, out_dtype=torch.float32)
     s = token_logprobs(logits, drafted, k=8)
 
-Rows are the first dimension; the last one is contiguous, rows may lie any stride apart.
+Rows are the first dimension; the last one is contiguous, rows may lie any stride apart.  The library takes vectors (weights,
+scales, biases) and ids that start on 16 bytes: slices that start elsewhere are copied for it.
 """
 from __future__ import annotations
 
@@ -56,10 +57,19 @@ def _rows(t: torch.Tensor, dev: int):
     return n, d, row if n > 1 else d       # torch leaves the stride of a dimension of one open
 
 
-def _vector(t: torch.Tensor, dev: int, n: int, dtype) -> int:
+def _start(t: torch.Tensor, held: list) -> int:
+    """Where t lies, or a copy of it that starts on 16 bytes, kept in `held` until the call has been made."""
+    p = t.data_ptr()
+    if p & 15:
+        held.append(t.clone())
+        p = held[-1].data_ptr()
+    return p
+
+
+def _vector(t: torch.Tensor, dev: int, n: int, dtype, held: list) -> int:
     assert t.get_device() == dev, "a call's tensors are on one GPU"
     assert t.dtype is dtype and t.shape == (n,) and t.is_contiguous()
-    return t.data_ptr()
+    return _start(t, held)
 
 
 def rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
@@ -69,6 +79,7 @@ def rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float =
     dev = _device(x)
     T, d, xs = _rows(x, dev)
     rp = sp = yp = qp = cp = total = out = q = scale = None
+    held = []
     rs = ss = 0
     where = x.device
     if residual is not None:
@@ -82,7 +93,7 @@ def rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float =
         sp = total.data_ptr()
     else:
         assert sum_out is None, "sum_out comes with a residual"
-    wp = None if weight is None else _vector(weight, dev, d, x.dtype)
+    wp = None if weight is None else _vector(weight, dev, d, x.dtype, held)
     if y:
         out = torch.empty((T, d), dtype=x.dtype, device=where)
         yp = out.data_ptr()
@@ -112,8 +123,9 @@ def linear_w8a8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
     M, K, a_row = _rows(a, dev)
     N, k, w_row = _rows(w, dev)
     assert a.dtype is _i8 and w.dtype is _i8 and k == K
-    sa, sw = _vector(a_scale, dev, M, _f32), _vector(w_scale, dev, N, _f32)
-    b = None if bias is None else _vector(bias, dev, N, _f32)
+    held = []
+    sa, sw = _vector(a_scale, dev, M, _f32, held), _vector(w_scale, dev, N, _f32, held)
+    b = None if bias is None else _vector(bias, dev, N, _f32, held)
     if out is None:
         out, out_row = torch.empty((M, N), dtype=out_dtype, device=a.device), N
     else:
@@ -135,13 +147,13 @@ def token_logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None, k: 
     probable tokens (equal logits: the lower id first), with entropy and lse."""
     dev = _device(logits)
     T, V, row = _rows(logits, dev)
-    n, ip, shape = 0, None, (T, 0)
+    n, ip, shape, held = 0, None, (T, 0), []
     if ids is not None:
         assert ids.get_device() == dev and ids.dtype is _i32 and ids.is_contiguous(), \
             "index tensors are contiguous int32 on the GPU of the call's other tensors"
         assert ids.dim() in (1, 2) and ids.shape[0] == T
         shape = ids.shape
-        n, ip = (1 if ids.dim() == 1 else shape[1]), ids.data_ptr()
+        n, ip = (1 if ids.dim() == 1 else shape[1]), _start(ids, held)
     where = logits.device
     logprob, entropy = torch.empty(shape, dtype=_f32, device=where), torch.empty(T, dtype=_f32, device=where)
     lse = torch.empty_like(entropy)
