@@ -443,8 +443,9 @@ __global__ void __launch_bounds__(kThreads, kResident) score_kernel(const ScoreA
     if (u.m == -INFINITY) return -INFINITY;
     if (u.m == INFINITY) return e == INFINITY ? nan : -INFINITY;
     const float d = e - u.M;
-    if (isinf(d) && !isinf(e)) return fmaf(__fmul_rn(0.5f * e - 0.5f * u.M, p.scale), 2.f, -lz);   // further apart than fp32 reaches
-    return fmaf(d, p.scale, -lz);
+    const float v = isinf(d) && !isinf(e) ? fmaf(__fmul_rn(0.5f * e - 0.5f * u.M, p.scale), 2.f, -lz)   // further apart than fp32 reaches
+                                          : fmaf(d, p.scale, -lz);
+    return v > 0.f ? 0.f : v;   // by rounding alone
   };
   if (tid < p.n_ids) p.logprob[asked] = id >= 0 && id < p.V ? logprob(logit) : nan;
   for (int i = tid + kThreads; i < p.n_ids; i += kThreads) {
@@ -454,7 +455,8 @@ __global__ void __launch_bounds__(kThreads, kResident) score_kernel(const ScoreA
   if (tid == 0) {
     const bool finite = fabsf(u.m) < INFINITY;
     if (p.lse) p.lse[row] = finite ? fmaf(u.M, p.scale, lz) : u.m;
-    if (p.entropy) p.entropy[row] = finite ? fmaf(-kLn2, u.s / u.z, lz) : (u.m == -INFINITY ? 0.f : nan);
+    const float h = fmaf(-kLn2, u.s / u.z, lz);
+    if (p.entropy) p.entropy[row] = finite ? (h < 0.f ? 0.f : h) : (u.m == -INFINITY ? 0.f : nan);
   }
   const int there = u.m == u.m ? min(p.k, p.V) : 0;
   for (int i = tid; i < PARTS * p.k; i += kThreads) {
