@@ -594,8 +594,11 @@ int moe_linear_w8a8(const int8_t *a, int64_t a_stride, const float *a_scale, con
  *   entropy[t] = -sum_j p_j ln p_j (terms with p_j = 0 are 0),   p_j = exp(scale x[t, j] - lse[t]),
  *   top_ids[t, :] = the k largest logits, descending, equal logits -> lower id; top_logprob[t, :] theirs.
  * logits: (T, V) F16 | BF16 | F32; ids: int32 (T, n_ids), ids outside [0, V) get NaN; all else fp32 or int32,
- * contiguous; entropy and lse may be NULL.  scale > 0 (a temperature's inverse), 0 <= k <= 64, T < 2^27, V < 2^30.  fp32 sums;
- * results are the same on every run.  entropy is never below 0, a log probability never above.
+ * contiguous; entropy and lse may be NULL.  scale > 0 (a temperature's inverse), 0 <= k <= 64, T < 2^27, V < 2^30.  fp32 sums
+ * of weights relative to a logit that is within a factor of 64 in weight of the row's largest: with e = 2^-24, lse and log
+ * probabilities are off by up to (V / 256 + 60) e and 8 e of the row's largest |scale x|, the entropy, a difference of two terms that may
+ * both be ln 64 larger than itself, by twice that sum's error times (1 + entropy) and 512 e.  Results are the same on every run.
+ * entropy is never below 0, a log probability never above.
  * Masked logits (-inf) have probability 0 and log probability -inf; they come last among the alternatives.  A row of nothing
  * but -inf gets lse = -inf, log probabilities of -inf and entropy 0.  Places past V get id -1 and -inf.  A row with a NaN gets NaN
  * everywhere and ids of -1.  A row with a +inf gets lse = inf, entropy NaN, -inf for finite logits and NaN for infinite ones. */
