@@ -127,6 +127,16 @@ __device__ __forceinline__ void store_four(const LinearArgs &p, bool vector, int
   }
 }
 
+// Whether `ok` holds in all 128 threads that share barrier `id`.
+__device__ __forceinline__ bool all_of_half(int id, bool ok) {
+  int all;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 q, %1, 0;\n bar.red.and.pred p, %2, 128, q;\n selp.s32 %0, 1, 0, p;\n}\n"
+               : "=r"(all)
+               : "r"(int(ok)), "r"(id)
+               : "memory");
+  return all != 0;
+}
+
 __global__ void __launch_bounds__(kTcThreads, 1)
     linear8_tc_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constant__ CUtensorMap map_w, const TcArgs t) {
   extern __shared__ __align__(1024) uint8_t dsmem[];
@@ -218,6 +228,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&d_empty[seg & 1]);
       }
+      // The half's four warps pass the barriers below together or not at all: one warp's wait may have been given up on (the CTA
+      // aborts) where another's has just been met, and the others would wait for it there without a limit.
+      if (t.splits == 1) ok = all_of_half(1 + half, ok);
       if (!ok) break;
       // 16 rows at a time through shared memory, so that a warp stores whole rows of the tile; with splits all rows stay there
       // (all of this CTA's MMAs are complete: the rows' ring is free).  Loops, not unrolled code: fetching instructions that are
