@@ -581,8 +581,8 @@ int moe_quantize_rows(const void *x, int64_t x_stride, int dtype, int64_t T, int
  * fp32 (N), bias fp32 (N) or NULL, out (M, N) F16 | BF16 | F32, apart from the inputs.  1 <= K <= 131071.  The result does not depend on M, on the
  * other rows or on which kernel runs: a token's outputs are the same bits alone and in any batch.
  * workspace: >= moe_linear_w8a8_workspace_size(M, N, K) bytes; one sized for M serves every call of fewer rows with the same N
- * and K.  Its contents have no influence.  Rows of w that do not all start on 16 bytes (K % 16 != 0 among them) are copied into it
- * on every call; where they do, the size for N = 0 is enough (none up to 16 rows). */
+ * and K.  Its contents have no influence.  Where K, w's start or its rows' stride (of more than one) is no multiple
+ * of 16, w is copied into it on every call; else the size for N = 0 is enough (none up to 16 rows). */
 size_t moe_linear_w8a8_workspace_size(int64_t M, int64_t N, int64_t K);
 int moe_linear_w8a8(const int8_t *a, int64_t a_stride, const float *a_scale, const int8_t *w, int64_t w_stride,
                     const float *w_scale, const float *bias, int64_t M, int64_t N, int64_t K, void *out,

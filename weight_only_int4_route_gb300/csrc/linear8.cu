@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) linear8_stream_kernel(const
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           // rows past the last one and values past a ragged end: zeros (f16 garbage could be NaN)
-          const bool there = 8 * t + g < rows && 64 * j + 16 * q < 64 * here;
+          const bool there = 8 * t + g < rows;
           const uint8_t *src = rp + (8 * t + g) * pitch + 128 * j;
           uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
           if (there && k - kStreamWarps * kChunk + 64 * j + 16 * q < end) {
@@ -247,8 +247,9 @@ template <int MT, int CT> int launch_stream(const LinearArgs &p, cudaStream_t st
   return check_launch("linear_w8a8");
 }
 
-// Rows up to which the weights are streamed past all of them at once.  24 rows there and on tcgen05: 4096 x 4096 15.7 and 11.6 us,
-// 6144 x 4096 25.0 and 15.3, 2048 x 2048 6.5 and 9.2; 16 rows 8.6, 13.4 and 5.2 there.
+// Rows up to which the weights are streamed past all of them at once, whatever N and K.  24 rows there and on tcgen05: 4096 x 4096
+// 15.7 and 11.6 us, 6144 x 4096 25.0 and 15.3, but 2048 x 2048 6.5 and 9.2: small weights would gain from the stream up to 24 rows.
+// 16 rows 8.6, 13.4 and 5.2 there.
 constexpr int64_t kStreamRows = 16;
 
 // The workspace: the rows as f16 (many rows), then the weights' rows padded to 16 bytes (if they need it).
