@@ -58,3 +58,23 @@ def test_a_small_eps_beside_small_rows(dense, dtype):  # noqa: F811
     for eps in (2.0 ** -40, 2.0 ** -100, 2.0 ** -120, 2.0 ** -149):
         n = dense.rmsnorm(on(x), None, eps, q8=True)
         check(n, x, None, eps)
+
+
+@pytest.mark.parametrize("dtype", WIDE)
+@pytest.mark.parametrize("d", LENGTHS)
+@pytest.mark.parametrize("eps", [1e-6, 1.5, 1e-27])
+@pytest.mark.parametrize("with_weight", [False, True])
+def test_small_rows_beside_an_eps(dense, dtype, d, eps, with_weight):  # noqa: F811
+    """eps covers the squares of rows whose products with the weight are subnormal: the codes and scales are v's all the same.  A
+    scale below the normal numbers is rounded once more, by half a step of 2^-149."""
+    row = draw(1, d, torch.float32, 8)[0]
+    sizes = (2.0 ** -58, 2.0 ** -62, 2.0 ** -100, 2.0 ** -124, 2.0 ** -131) + ((2.0 ** -140, 2.0 ** -147) if dtype is torch.float32 else ())
+    x = torch.stack([(row.double() * s).float() for s in sizes] + [row * 0]).to(dtype)
+    weight = (1 + 0.2 * draw(1, d, torch.float32, 7)[0].clamp(-3, 3)).to(dtype) if with_weight else None
+    n = dense.rmsnorm(on(x), None if weight is None else on(weight), eps, q8=True)
+    v = D.rmsnorm(x, None, weight, torch.tensor(eps, dtype=torch.float32).double())[1]
+    half_step = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps / 2
+    assert ((n.y.double().cpu() - v).abs() <= (U[dtype] + 48 * E) * v.abs() + half_step + 3 * 2.0 ** -150).all()
+    steps, scale = D.steps8(v)
+    assert ((n.scale.double().cpu() - scale).abs() <= 48 * E * scale + 2.0 ** -150).all()
+    assert ((n.q.double().cpu() - steps).abs() <= 0.5 + 127 * 6 * E).all()

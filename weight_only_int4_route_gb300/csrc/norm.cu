@@ -115,7 +115,7 @@ __device__ __forceinline__ void row_reduce(float &ss, float &top, int lanes, Exc
 // A row per `lanes` threads, NV vectors of V elements a thread; Q8: with 8-bit output.
 // SV (with V = 1): rows that could be read 16 bytes, SV elements, at a time if they lay otherwise.  Their squares are added up in the
 // order that they have there (from shared memory, in fp32), so a row's result does not depend on where it lies.  In bf16 with
-// residual and 8-bit output: 8192 rows of 4096 at odd starts 121 us (16-byte starts 40), 5000 rows of 256 6.5 us (an
+// residual and 8-bit output: 8192 rows of 4096 at odd starts 117 us (16-byte starts 40), 5000 rows of 256 6.2 us (an
 // order of their own 5.8).
 template <typename T, int V, int NV, int MOST, bool Q8, int SV>
 __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs p) {
@@ -238,17 +238,17 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs p) {
   }
   if (Q8) {
     const bool fine = top <= 3.402823466e38f;   // neither infinite nor NaN
-    float step = 0.f, up = 1.f;
-    if (top > 0.f && fine) {
-      if (top < 0x1p-60f) {   // 127 / top overflows below 2^-121: small rows are brought up first (exact)
-        up = 0x1p60f;
+    const float largest = top;
+    float step = 0.f;
+    const bool small = top < 0x1p-60f;
+    if (small) {   // 127 / top overflows below 2^-121, products with the weight lose bits or all below 2^-126: the row is brought up first
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int j = 0; j < V; ++j) h[i][j] *= up;
-      }
-      step = __fdiv_rn(127.f, top * up);
+        for (int j = 0; j < V; ++j) h[i][j] *= 0x1p60f;
+      reduce();
     }
+    if (top > 0.f && fine) step = __fdiv_rn(127.f, top);
     int8_t *q = p.q + row * p.d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -260,7 +260,11 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs p) {
       for (int j = 0; j < V; ++j) c[j] = fine ? __float_as_uint(__fadd_rn(__fmul_rn(h[i][j] * f[j], step), 12582912.f)) : 0;
       if (at(i) < p.d) P::store_codes(q + at(i), c);
     }
-    if (t == 0) p.scale[row] = !fine ? __int_as_float(0x7fc00000) : (top > 0.f ? __fdiv_rn(top, 127.f) * r : 0.f);
+    if (t == 0) {
+      float scale = __fdiv_rn(largest, 127.f) * r;
+      if (small && p.norm) scale = __fdiv_rn(top * r, 127.f) * 0x1p-60f;   // one rounding where the scale is subnormal
+      p.scale[row] = !fine ? __int_as_float(0x7fc00000) : (top > 0.f ? scale : 0.f);
+    }
   }
 }
 
